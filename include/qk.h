@@ -52,6 +52,15 @@ extern "C" {
 #define QK_TYPE_Q6_K 14
 #define QK_TYPE_Q8_K 15
 
+/* Element types of the attention calls' float tensors (ggml ids; not block types). */
+#define QK_TYPE_F32 0
+#define QK_TYPE_F16 1
+#define QK_TYPE_BF16 30
+
+/* Which dims of a head form the pairs that qk_kv_append rotates. */
+#define QK_ROPE_HALVES 0 /* dim i with dim i + n_rot / 2 */
+#define QK_ROPE_PAIRS 1  /* dim 2 i with dim 2 i + 1 */
+
 /* Status codes returned by every call that can fail. */
 #define QK_OK 0
 #define QK_E_TYPE 1   /* unknown type id, or a type the call does not take */
@@ -272,6 +281,141 @@ int qk_gemv_pair(int w_type, const void* W1, const void* W2, int64_t n_out, int6
 int qk_gemv_pair_timed(int w_type, const void* W1, const void* W2, int64_t n_out, int64_t n_in,
                        const void* xq, int64_t ncols, int epilogue, float* out, void* stream,
                        void* ev_start, void* ev_stop);
+
+/*
+ * The 4-bit KV cache and the attention around it.
+ *
+ * Keys and values are cached in Q4_0 blocks (32 dims of one head, f16 scale, value
+ * scale * (code - 8), the rule of qk_quantize_row) in pages of a caller's buffer:
+ * uint8 [n_pages][n_kv_heads][qk_kv_page_bytes(...)], 16-byte aligned.  One page of one head, T =
+ * page_tokens, D = head_dim:
+ *   K codes   T rows of D / 2 bytes      K scales  T rows of D / 32 f16
+ *   V codes   T rows of D / 2 bytes      V scales  T rows of D / 32 f16
+ * A code row is 4 groups g of D / 32 little-endian dwords b; dword (g, b) holds dims
+ * 32 b + 8 g + j, j = 0..7: nibble n, counted from the low end, is j = 2 n for n < 4 and
+ * j = 2 (n - 4) + 1 for n >= 4.  These are the codes and scale of the Q4_0 block in an order
+ * of the cache's own; the cache is not a file format.
+ *
+ * qk_kv_batch says which rows a call works on and where they lie: row r of the packed
+ * tensors with cu[i] <= r < cu[i + 1] belongs to sequence i and is its cache position
+ * start[i] + r - cu[i], which lies in page page_table[i][position / page_tokens], slot
+ * position % page_tokens.  The index arrays are device memory, 4-byte aligned, read
+ * by the kernels when they run, so a captured graph follows their contents.  A row outside
+ * every sequence, a negative position, a position beyond the table and a table entry
+ * outside 0 .. n_pages - 1 are never followed: what each call does with such a row is
+ * stated at the call.  Sequences that write to one page slot in one call leave one of
+ * the rows there.
+ */
+typedef struct qk_kv_batch {
+  int32_t type;              /* QK_TYPE_Q4_0 (else QK_E_TYPE) */
+  int32_t page_tokens;       /* 16, 32, 64, 128 or 256 (else QK_E_ARG) */
+  int64_t n_pages;           /* pages in the buffer, >= 0, <= INT32_MAX */
+  int64_t n_kv_heads;        /* 1 .. 1024 */
+  int64_t head_dim;          /* 64, 96, 128 or 256 (else QK_E_SHAPE) */
+  const int32_t* page_table; /* [n_seq][max_pages] */
+  int64_t max_pages;         /* >= 0, <= INT32_MAX / page_tokens */
+  const int32_t* cu;         /* [n_seq + 1], ascending */
+  const int32_t* start;      /* [n_seq] */
+  int64_t n_seq;             /* >= 0, <= INT32_MAX / 64 */
+  int64_t n_rows;            /* packed rows, >= 0, <= INT32_MAX / 1024; 0 enqueues nothing */
+} qk_kv_batch;
+
+/* Bytes of one page of one head, K and V: page_tokens * (head_dim + head_dim / 8), 0 when
+ * the type, page_tokens or head_dim is none that the cache takes. */
+int64_t qk_kv_page_bytes(int type, int64_t page_tokens, int64_t head_dim);
+
+/*
+ * qk_kv_append - rotate new query and key rows by their position, quantize the keys and
+ * values and write them to their pages.
+ *   pages      the cache, written.
+ *   dtype      QK_TYPE_F32, QK_TYPE_F16 or QK_TYPE_BF16 (else QK_E_TYPE): k, v, q, q_out.
+ *   k, v       rows of n_kv_heads * head_dim elements, k_stride / v_stride elements
+ *              apart (a slice of a fused projection's output will do).
+ *   q          rows of n_heads * head_dim elements q_stride apart, or NULL: no queries.
+ *   n_heads    query heads, 1 .. 1024 (with q NULL: ignored).
+ *   rope       f32 [rope_rows][n_rot / 2][2]: cos and sin of each pair's angle at each
+ *              position (NULL with n_rot 0).
+ *   n_rot      dims of each head that are rotated, from the first: 0 or a multiple of 16
+ *              up to head_dim (else QK_E_SHAPE).
+ *   rope_style QK_ROPE_HALVES or QK_ROPE_PAIRS (else QK_E_ARG).
+ *   q_out      out: [n_rows][n_heads][head_dim], the rotated queries; its range must not
+ *              overlap q's (QK_E_ARG).
+ * Rotation of a pair (a, b): fl(fl(a cos) - fl(b sin)) and fl(fl(a sin) + fl(b cos)) in f32,
+ * every operation rounded on its own.  Keys are quantized from those f32 values, queries are
+ * rounded once to dtype.  The codes and scales are qk_quantize_row's of the same
+ * f32 values, bit for bit.  Inputs must be finite.
+ * A row whose position is not in the rope table (n_rot > 0) or which lies outside every
+ * sequence is left out: nothing is written for it.  A row without a valid page
+ * writes its query only.
+ * Errors: QK_E_TYPE; QK_E_ARG; QK_E_SHAPE (a size outside its range, n_heads not a multiple of
+ * n_kv_heads, a row stride shorter than a row); QK_E_NULL; QK_E_ALIGN (a float tensor's base
+ * or row stride not a multiple of 16 bytes); QK_E_LIMIT; QK_E_DEVICE.
+ */
+int qk_kv_append(const qk_kv_batch* batch, void* pages, int dtype, const void* k, int64_t k_stride,
+                 const void* v, int64_t v_stride, const void* q, int64_t q_stride, int64_t n_heads,
+                 const float* rope, int64_t rope_rows, int64_t n_rot, int rope_style, void* q_out,
+                 void* stream);
+
+/*
+ * qk_kv_read - read cached rows back as float values: d * (code - 8), rounded once to
+ * dtype.  For a long prompt taken in chunks: read positions 0 .. back (the cached
+ * prefix and the chunk just appended) and run qk_attn_prompt on them.
+ *   k_out, v_out  out: dtype [n_rows][n_kv_heads][head_dim].
+ * A row without a valid page gives zeros; a row outside every sequence is not written.
+ * Errors as qk_kv_append.
+ */
+int qk_kv_read(const qk_kv_batch* batch, const void* pages, int dtype, void* k_out, void* v_out,
+               void* stream);
+
+/* Bytes of workspace that qk_attn_paged needs for a batch and a number of query heads
+ * (a function of the counts in the batch, not of the index arrays' contents; may be 0).
+ * 0 too when the batch is one that qk_attn_paged refuses. */
+int64_t qk_attn_paged_ws_bytes(const qk_kv_batch* batch, int64_t n_heads);
+
+/*
+ * qk_attn_paged - attention of query rows over the cache: for each row and head the
+ * softmax of scale * q . k over the positions up to the row's own (which
+ * has been appended before), applied to the values.  One row per sequence is a decode step, a few
+ * are drafted tokens to verify or a short chunk; for long chunks qk_kv_read and qk_attn_prompt
+ * are the faster pair.
+ *   dtype     QK_TYPE_F32, QK_TYPE_F16 or QK_TYPE_BF16 (else QK_E_TYPE): q and out.
+ *   q         rows of n_heads * head_dim elements q_stride apart; query head h reads
+ *             key / value head h / (n_heads / n_kv_heads).
+ *   n_heads   a multiple of n_kv_heads, <= 1024 (else QK_E_SHAPE).
+ *   scale     finite (else QK_E_ARG).
+ *   window    0, or the number of positions a row sees, its own the last (< 0: QK_E_ARG).
+ *   out       out: [n_rows][n_heads][head_dim]; its range must not overlap q's (QK_E_ARG).
+ *   ws        qk_attn_paged_ws_bytes bytes, 16-byte aligned; too few: QK_E_ARG.
+ * Scores, softmax statistics and sums are f32; with f16 and bf16 the softmax weights are rounded
+ * to f16 for the matrix cores.  Positions without a valid page count as masked.
+ * A row that sees nothing gives zeros; a row outside every sequence is not written.
+ * Errors otherwise as qk_kv_append.
+ */
+int qk_attn_paged(const qk_kv_batch* batch, const void* pages, int dtype, const void* q, int64_t q_stride,
+                  int64_t n_heads, float scale, int64_t window, void* out, void* ws, int64_t ws_bytes,
+                  void* stream);
+
+/*
+ * qk_attn_prompt - attention over packed prompts held as float q, k and v.
+ *   dtype     QK_TYPE_F32, QK_TYPE_F16 or QK_TYPE_BF16 (else QK_E_TYPE).
+ *   q         n_q rows of n_heads * head_dim elements q_stride apart; k, v: n_k
+ *             rows of n_kv_heads * head_dim elements (heads as qk_attn_paged).
+ *   cu_q, cu_k  device int32 [n_seq + 1], ascending: sequence i is q rows
+ *             cu_q[i] .. cu_q[i + 1] - 1 and keys cu_k[i] .. cu_k[i + 1] - 1.  The last
+ *             query row stands at the last key: row r of Lq stands at key r + Lk - Lq.
+ *   causal    1: a row sees no key behind its own place; 0: it sees all (else QK_E_ARG).
+ *   window    0, or: a row sees no key `window` or more places before its own.
+ *   out       out: [n_q][n_heads][head_dim]; its range must not overlap q's (QK_E_ARG).
+ * n_q, n_k <= INT32_MAX / 1024.  Scores, softmax statistics and sums are f32; with f16 and
+ * bf16 the softmax weights are rounded to that type for the matrix cores.  A row that
+ * sees no key gives zeros; a row outside every sequence is not written; keys outside
+ * 0 .. n_k - 1 are not read.  n_q = 0 enqueues nothing.
+ * Errors as qk_attn_paged.
+ */
+int qk_attn_prompt(int dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k,
+                   int64_t n_seq, int64_t n_q, int64_t n_k, int64_t n_heads, int64_t n_kv_heads,
+                   int64_t head_dim, float scale, int causal, int64_t window, void* out, void* stream);
 
 /*
  * qk_read_probe - measurement probe, not part of the method: a kernel that only

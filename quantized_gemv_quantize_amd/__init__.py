@@ -1,10 +1,12 @@
-"""MI355X block-quantized GEMV (ggml Q8_0 / Q4_0 / Q5_0 / Q4_K / Q5_K / Q6_K) - Python binding.
+"""MI355X block-quantized GEMV (ggml Q8_0 / Q4_0 / Q5_0 / Q4_K / Q5_K / Q6_K), 4-bit paged KV
+cache and attention - Python binding.
 
 A thin ctypes binding over libqk.so (C ABI in include/qk.h).  Functions carry
 the C names and only marshal arguments: torch tensors supply device pointers
 and the current stream; every step of the computation runs in the HIP kernels.
 There is no fallback: if libqk.so is missing or cannot be loaded, calls raise.
 """
+import contextlib
 import ctypes
 import os
 
@@ -24,6 +26,11 @@ WEIGHT_TYPES = (QK_TYPE_Q8_0, QK_TYPE_Q4_0, QK_TYPE_Q5_0, QK_TYPE_Q4_1, QK_TYPE_
                 QK_TYPE_Q3_K, QK_TYPE_Q4_K, QK_TYPE_Q5_K, QK_TYPE_Q6_K)
 DEQUANT_TYPES = WEIGHT_TYPES
 QUANT_ROW_TYPES = (QK_TYPE_Q8_0, QK_TYPE_Q4_0, QK_TYPE_Q4_1, QK_TYPE_Q5_0)
+QK_TYPE_F32 = 0
+QK_TYPE_F16 = 1
+QK_TYPE_BF16 = 30
+QK_ROPE_HALVES = 0
+QK_ROPE_PAIRS = 1
 QK_EPI_NONE = 0
 QK_EPI_SWIGLU = 1
 TYPE_NAMES = {QK_TYPE_Q4_0: "Q4_0", QK_TYPE_Q4_1: "Q4_1", QK_TYPE_Q5_0: "Q5_0", QK_TYPE_Q5_1: "Q5_1",
@@ -36,6 +43,14 @@ DEFAULT_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib
 LIB_PATH = os.environ.get("QK_LIB_PATH") or DEFAULT_LIB_PATH
 
 _lib = None
+
+
+class _KVBatch(ctypes.Structure):
+    """qk_kv_batch of include/qk.h."""
+    _fields_ = [("type", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int64), ("cu", ctypes.c_void_p), ("start", ctypes.c_void_p),
+                ("n_seq", ctypes.c_int64), ("n_rows", ctypes.c_int64)]
 
 
 class QKError(RuntimeError):
@@ -87,6 +102,20 @@ def lib():
         L.qk_gemv_pair.argtypes = [i32, p, p, i64, i64, p, i64, i32, p, p]
         L.qk_gemv_pair_timed.restype = i32
         L.qk_gemv_pair_timed.argtypes = [i32, p, p, i64, i64, p, i64, i32, p, p, p, p]
+        b, f32 = ctypes.POINTER(_KVBatch), ctypes.c_float
+        L.qk_kv_page_bytes.restype = i64
+        L.qk_kv_page_bytes.argtypes = [i32, i64, i64]
+        L.qk_kv_append.restype = i32
+        L.qk_kv_append.argtypes = [b, p, i32, p, i64, p, i64, p, i64, i64, p, i64, i64, i32, p, p]
+        L.qk_kv_read.restype = i32
+        L.qk_kv_read.argtypes = [b, p, i32, p, p, p]
+        L.qk_attn_paged_ws_bytes.restype = i64
+        L.qk_attn_paged_ws_bytes.argtypes = [b, i64]
+        L.qk_attn_paged.restype = i32
+        L.qk_attn_paged.argtypes = [b, p, i32, p, i64, i64, f32, i64, p, p, i64, p]
+        L.qk_attn_prompt.restype = i32
+        L.qk_attn_prompt.argtypes = [i32, p, i64, p, i64, p, i64, p, p, i64, i64, i64, i64, i64, i64, f32, i32, i64,
+                                     p, p]
         L.qk_read_probe.restype = i32
         L.qk_read_probe.argtypes = [p, i64, p, p, p, p]
         L.qk_read_probe_ex.restype = i32
@@ -246,6 +275,141 @@ def qk_gemv_pair_timed(w_type, W1, W2, n_out, n_in, xq, ncols, epilogue, out, ev
     _check(lib().qk_gemv_pair_timed(w_type, _ptr(W1), _ptr(W2), n_out, n_in, _ptr(xq), ncols,
                                     epilogue, _ptr(out), _stream(stream), e0, e1),
            "qk_gemv_pair_timed")
+    return out
+
+
+def _float_type(dtype):
+    import torch
+    t = {torch.float32: QK_TYPE_F32, torch.float16: QK_TYPE_F16, torch.bfloat16: QK_TYPE_BF16}.get(dtype)
+    if t is None:
+        raise TypeError(f"dtype {dtype}: the attention calls take float32, float16 and bfloat16")
+    return t
+
+
+def _heads(t, what, dtype):
+    """(rows, heads, head dim, row stride) of a [rows, heads, D] tensor whose rows may be strided."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} is {t.dtype}, not {dtype}")
+    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
+        raise ValueError(f"{what}: [rows, heads, head dim] with contiguous rows, not shape {tuple(t.shape)} "
+                         f"strides {t.stride()}")
+    n, h, d = t.shape
+    return n, h, d, t.stride(0) if n > 1 else h * d
+
+
+def _index(t, what, shape):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 {list(shape)}, not {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _result(t, what, shape, like, dtype):
+    """The caller's output tensor, checked, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    return t
+
+
+def _kv_batch(pages, page_tokens, page_table, cu, start, n_rows, head_dim):
+    import torch
+    if pages.dtype != torch.uint8 or pages.dim() != 3 or not pages.is_contiguous() or \
+            pages.shape[2] != page_tokens * (head_dim + head_dim // 8):
+        raise ValueError(f"pages: contiguous uint8 [pages, kv heads, {page_tokens * (head_dim + head_dim // 8)}], not "
+                         f"{pages.dtype} {list(pages.shape)}")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: int32 [sequences, pages], not {list(page_table.shape)}")
+    n_seq, max_pages = page_table.shape
+    return _KVBatch(QK_TYPE_Q4_0, page_tokens, pages.shape[0], pages.shape[1], head_dim,
+                    _index(page_table, "page_table", (n_seq, max_pages)), max_pages, _index(cu, "cu", (n_seq + 1,)),
+                    _index(start, "start", (n_seq,)), n_seq, n_rows)
+
+
+def qk_kv_page_bytes(t, page_tokens, head_dim):
+    return int(lib().qk_kv_page_bytes(t, page_tokens, head_dim))
+
+
+def qk_kv_append(pages, page_tokens, page_table, cu, start, k, v, q=None, rope=None, rope_style=QK_ROPE_HALVES,
+                 q_out=None, stream=None):
+    """Rotates the rows of q and k ([rows, heads, D], rows may be strided) by their position, quantizes
+    k and v to Q4_0 and writes them to the cache `pages` (uint8 [pages, kv heads, page bytes], in place).
+    page_table int32 [sequences, pages], cu int32 [sequences + 1] and start int32 [sequences] say
+    where the rows go.  rope: f32 [positions, n_rot / 2, 2] (cos, sin), None for no rotation.
+    Returns the rotated queries, None without q."""
+    import torch
+    n, hk, d, ks = _heads(k, "k", k.dtype)
+    nv, hv, dv, vs = _heads(v, "v", k.dtype)
+    if (nv, hv, dv) != (n, hk, d) or hk != pages.shape[1]:
+        raise ValueError(f"k {list(k.shape)}, v {list(v.shape)}, pages {list(pages.shape)}")
+    b = _kv_batch(pages, page_tokens, page_table, cu, start, n, d)
+    t, h, qs = _float_type(k.dtype), 0, 0
+    if q is not None:
+        nq, h, dq, qs = _heads(q, "q", k.dtype)
+        if (nq, dq) != (n, d):
+            raise ValueError(f"q {list(q.shape)}, k {list(k.shape)}")
+        q_out = _result(q_out, "q_out", (n, h, d), q, k.dtype)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or
+                             not rope.is_contiguous()):
+        raise ValueError(f"rope: contiguous float32 [positions, n_rot / 2, 2], not {rope.dtype} {list(rope.shape)}")
+    rows, rot = (rope.shape[0], 2 * rope.shape[1]) if rope is not None else (0, 0)
+    _check(lib().qk_kv_append(b, pages.data_ptr(), t, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, h, _ptr(rope), rows,
+                              rot, rope_style, _ptr(q_out), _stream(stream)), "qk_kv_append")
+    return q_out
+
+
+def qk_kv_read(pages, page_tokens, page_table, cu, start, n_rows, head_dim, dtype=None, k_out=None, v_out=None,
+               stream=None):
+    """(k, v), each [n_rows, kv heads, head_dim] of `dtype` (float32 where none is given), of cached rows."""
+    import torch
+    dtype = dtype or (k_out.dtype if k_out is not None else torch.float32)
+    b = _kv_batch(pages, page_tokens, page_table, cu, start, n_rows, head_dim)
+    shape = (n_rows, pages.shape[1], head_dim)
+    k_out = _result(k_out, "k_out", shape, pages, dtype)
+    v_out = _result(v_out, "v_out", shape, pages, dtype)
+    _check(lib().qk_kv_read(b, pages.data_ptr(), _float_type(dtype), k_out.data_ptr(), v_out.data_ptr(),
+                            _stream(stream)), "qk_kv_read")
+    return k_out, v_out
+
+
+def qk_attn_paged(pages, page_tokens, page_table, cu, start, q, scale=None, window=0, out=None, ws=None, stream=None):
+    """Attention of the rows of q [rows, heads, D] over the cache up to each row's own position; scale
+    is 1 / sqrt(D) where none is given.  ws: a uint8 workspace to reuse (allocated when None)."""
+    import torch
+    n, h, d, qs = _heads(q, "q", q.dtype)
+    b = _kv_batch(pages, page_tokens, page_table, cu, start, n, d)
+    out = _result(out, "out", (n, h, d), q, q.dtype)
+    need = int(lib().qk_attn_paged_ws_bytes(b, h))
+    if ws is None and need:
+        # the allocator ties the workspace to the stream that is current here
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    _check(lib().qk_attn_paged(b, pages.data_ptr(), _float_type(q.dtype), q.data_ptr(), qs, h,
+                               d ** -0.5 if scale is None else scale, window, out.data_ptr(), _ptr(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "qk_attn_paged")
+    return out
+
+
+def qk_attn_prompt(q, k, v, cu_q, cu_k=None, scale=None, causal=True, window=0, out=None, stream=None):
+    """Attention over packed prompts: q [rows, heads, D], k and v [keys, kv heads, D] (rows may be strided),
+    cu_q and cu_k int32 [sequences + 1] (one for both where cu_k is not given); scale is
+    1 / sqrt(D) where none is given."""
+    n, h, d, qs = _heads(q, "q", q.dtype)
+    nk, hk, dk, ks = _heads(k, "k", q.dtype)
+    nv, hv, dv, vs = _heads(v, "v", q.dtype)
+    if (nv, hv, dv) != (nk, hk, d) or dk != d or (cu_k is None and nk != n):
+        raise ValueError(f"q {list(q.shape)}, k {list(k.shape)}, v {list(v.shape)}")
+    n_seq = cu_q.numel() - 1
+    pq = _index(cu_q, "cu_q", (n_seq + 1,))
+    pk = pq if cu_k is None else _index(cu_k, "cu_k", (n_seq + 1,))
+    out = _result(out, "out", (n, h, d), q, q.dtype)
+    _check(lib().qk_attn_prompt(_float_type(q.dtype), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, pq, pk, n_seq, n,
+                                nk, h, hk, d, d ** -0.5 if scale is None else scale, int(causal), window,
+                                out.data_ptr(), _stream(stream)), "qk_attn_prompt")
     return out
 
 

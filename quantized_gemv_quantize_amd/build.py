@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqk.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["qk_capi.hip", "qk_quantize.hip", "qk_gemv.hip", "qk_gemm.hip", "qk_dequant.hip",
-           "qk_probe.hip"]
+           "qk_probe.hip", "qk_kv.hip", "qk_attn_paged.hip", "qk_attn_prompt.hip"]
 ARCH = "gfx950"
 
 

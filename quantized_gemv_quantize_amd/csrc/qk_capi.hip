@@ -5,8 +5,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "../../include/qk.h"
 #include "qk_internal.h"
+#include "qk_kv.h"
 
 namespace {
 
@@ -109,6 +112,61 @@ int gemv_impl(int w_type, const void* W, int64_t n_out, int64_t n_in, const void
     if (e != hipSuccess) return status_of(e);
   }
   return QK_OK;
+}
+
+// Bytes per element of an attention call's float type, 0 for any other id.
+int64_t float_bytes(int dtype) {
+  return dtype == QK_TYPE_F32 ? 4 : (dtype == QK_TYPE_F16 || dtype == QK_TYPE_BF16) ? 2 : 0;
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool is_head_dim(int64_t d) { return d == 64 || d == 96 || d == 128 || d == 256; }
+bool is_page(int64_t t) { return t == 16 || t == 32 || t == 64 || t == 128 || t == 256; }
+
+// Head counts and row counts beyond which an index of a kernel could leave 32 bits.
+constexpr int64_t kMaxHeads = 1024;
+constexpr int64_t kMaxRows = INT32_MAX / 1024;
+// Row strides of the float tensors, in elements (32 times the widest row): with kMaxRows a byte offset stays far inside 64 bits.
+constexpr int64_t kMaxStride = int64_t(1) << 23;
+
+// One float operand: rows of `width` elements `stride` apart.
+int check_rows(const void* p, int64_t stride, int64_t width, int64_t es) {
+  if (stride < width || stride > kMaxStride) return QK_E_SHAPE;
+  if (p == nullptr) return QK_E_NULL;
+  if (!aligned16(p) || stride * es % 16 != 0) return QK_E_ALIGN;
+  return QK_OK;
+}
+
+// Whether the byte ranges of `rows` rows at p (strided) and at o (contiguous) meet.
+bool overlaps(const void* p, int64_t stride, const void* o, int64_t width, int64_t rows, int64_t es) {
+  const uintptr_t p0 = reinterpret_cast<uintptr_t>(p), o0 = reinterpret_cast<uintptr_t>(o);
+  return p0 < o0 + rows * width * es && o0 < p0 + ((rows - 1) * stride + width) * es;
+}
+
+// The counts and, where rows are to be worked on, the pointers of a batch.
+int check_batch(const qk_kv_batch* b, qk::KvBatch* out) {
+  if (b == nullptr) return QK_E_NULL;
+  if (b->type != QK_TYPE_Q4_0) return QK_E_TYPE;
+  if (!is_page(b->page_tokens)) return QK_E_ARG;
+  if (!is_head_dim(b->head_dim) || b->n_kv_heads < 1 || b->n_kv_heads > kMaxHeads) return QK_E_SHAPE;
+  if (b->n_pages < 0 || b->n_pages > INT32_MAX || b->max_pages < 0 || b->max_pages > INT32_MAX / b->page_tokens)
+    return QK_E_SHAPE;
+  if (b->n_seq < 0 || b->n_seq > INT32_MAX / 64 || b->n_rows < 0 || b->n_rows > kMaxRows) return QK_E_SHAPE;
+  int shift = 0;
+  while ((1 << shift) < b->page_tokens) ++shift;
+  *out = qk::KvBatch{b->page_table, b->cu, b->start, b->max_pages, b->n_pages, b->n_rows,
+                     static_cast<int>(b->n_seq), static_cast<int>(b->n_kv_heads), shift};
+  return QK_OK;
+}
+
+int check_batch_memory(const qk_kv_batch* b, const void* pages) {
+  if (b->cu == nullptr || b->start == nullptr || (b->page_table == nullptr && b->max_pages > 0)) return QK_E_NULL;
+  if (pages == nullptr && b->n_pages > 0) return QK_E_NULL;
+  if (!aligned4(b->cu) || !aligned4(b->start) || !aligned4(b->page_table) || !aligned16(pages)) return QK_E_ALIGN;
+  return QK_OK;
+}
+
+bool heads_ok(int64_t n_heads, int64_t n_kv) {
+  return n_heads >= 1 && n_heads <= kMaxHeads && n_kv >= 1 && n_heads % n_kv == 0;
 }
 
 }  // namespace
@@ -308,6 +366,109 @@ int qk_read_probe_ex(const void* src, int64_t bytes, uint32_t* out, int kb_per_w
 int qk_read_probe(const void* src, int64_t bytes, uint32_t* out, void* stream, void* ev_start,
                   void* ev_stop) {
   return qk_read_probe_ex(src, bytes, out, 2, 0, 0, stream, ev_start, ev_stop);
+}
+
+int64_t qk_kv_page_bytes(int type, int64_t page_tokens, int64_t head_dim) {
+  if (type != QK_TYPE_Q4_0 || !is_page(page_tokens) || !is_head_dim(head_dim)) return 0;
+  return 2 * qk::kv_half_bytes(page_tokens, head_dim);
+}
+
+int qk_kv_append(const qk_kv_batch* batch, void* pages, int dtype, const void* k, int64_t k_stride, const void* v,
+                 int64_t v_stride, const void* q, int64_t q_stride, int64_t n_heads, const float* rope,
+                 int64_t rope_rows, int64_t n_rot, int rope_style, void* q_out, void* stream) {
+  qk::KvBatch b;
+  int rc = check_batch(batch, &b);
+  if (rc != QK_OK) return rc;
+  const int64_t es = float_bytes(dtype), dim = batch->head_dim, kv_width = batch->n_kv_heads * dim;
+  if (es == 0) return QK_E_TYPE;
+  if (rope_style != QK_ROPE_HALVES && rope_style != QK_ROPE_PAIRS) return QK_E_ARG;
+  if (n_rot < 0 || n_rot > dim || n_rot % 16 != 0 || rope_rows < 0 || rope_rows > INT32_MAX) return QK_E_SHAPE;
+  if (q != nullptr && !heads_ok(n_heads, batch->n_kv_heads)) return QK_E_SHAPE;
+  if (batch->n_rows == 0) return QK_OK;
+  if ((rc = check_batch_memory(batch, pages)) != QK_OK) return rc;
+  if ((rc = check_rows(k, k_stride, kv_width, es)) != QK_OK) return rc;
+  if ((rc = check_rows(v, v_stride, kv_width, es)) != QK_OK) return rc;
+  if (n_rot > 0 && rope == nullptr) return QK_E_NULL;
+  if (n_rot > 0 && !aligned16(rope)) return QK_E_ALIGN;
+  if (q != nullptr) {
+    if ((rc = check_rows(q, q_stride, n_heads * dim, es)) != QK_OK) return rc;
+    if ((rc = check_rows(q_out, n_heads * dim, n_heads * dim, es)) != QK_OK) return rc;
+    if (overlaps(q, q_stride, q_out, n_heads * dim, batch->n_rows, es)) return QK_E_ARG;
+  }
+  return status_of(qk::launch_kv_append(b, static_cast<int>(dim), dtype, static_cast<uint8_t*>(pages), k, k_stride, v,
+                                        v_stride, q, q_stride, q != nullptr ? static_cast<int>(n_heads) : 0, rope,
+                                        rope_rows, static_cast<int>(n_rot), rope_style == QK_ROPE_HALVES, q_out,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int qk_kv_read(const qk_kv_batch* batch, const void* pages, int dtype, void* k_out, void* v_out, void* stream) {
+  qk::KvBatch b;
+  int rc = check_batch(batch, &b);
+  if (rc != QK_OK) return rc;
+  if (float_bytes(dtype) == 0) return QK_E_TYPE;
+  if (batch->n_rows == 0) return QK_OK;
+  if ((rc = check_batch_memory(batch, pages)) != QK_OK) return rc;
+  if (k_out == nullptr || v_out == nullptr) return QK_E_NULL;
+  if (!aligned16(k_out) || !aligned16(v_out)) return QK_E_ALIGN;
+  return status_of(qk::launch_kv_read(b, static_cast<int>(batch->head_dim), dtype, static_cast<const uint8_t*>(pages),
+                                      k_out, v_out, static_cast<hipStream_t>(stream)));
+}
+
+int64_t qk_attn_paged_ws_bytes(const qk_kv_batch* batch, int64_t n_heads) {
+  qk::KvBatch b;
+  if (check_batch(batch, &b) != QK_OK || !heads_ok(n_heads, batch->n_kv_heads) || batch->n_rows == 0) return 0;
+  return qk::attn_paged_ws_bytes(b, static_cast<int>(batch->head_dim), static_cast<int>(n_heads));
+}
+
+int qk_attn_paged(const qk_kv_batch* batch, const void* pages, int dtype, const void* q, int64_t q_stride,
+                  int64_t n_heads, float scale, int64_t window, void* out, void* ws, int64_t ws_bytes, void* stream) {
+  qk::KvBatch b;
+  int rc = check_batch(batch, &b);
+  if (rc != QK_OK) return rc;
+  const int64_t es = float_bytes(dtype), dim = batch->head_dim;
+  if (es == 0) return QK_E_TYPE;
+  if (!heads_ok(n_heads, batch->n_kv_heads)) return QK_E_SHAPE;
+  const int64_t width = n_heads * dim;
+  if (!std::isfinite(scale) || window < 0) return QK_E_ARG;
+  if (batch->n_rows == 0) return QK_OK;
+  if ((rc = check_batch_memory(batch, pages)) != QK_OK) return rc;
+  if ((rc = check_rows(q, q_stride, width, es)) != QK_OK) return rc;
+  if ((rc = check_rows(out, width, width, es)) != QK_OK) return rc;
+  if (overlaps(q, q_stride, out, width, batch->n_rows, es)) return QK_E_ARG;
+  const int64_t need = qk::attn_paged_ws_bytes(b, static_cast<int>(dim), static_cast<int>(n_heads));
+  if (need > 0 && ws == nullptr) return QK_E_NULL;
+  if (need > 0 && !aligned16(ws)) return QK_E_ALIGN;
+  if (ws_bytes < need) return QK_E_ARG;
+  return status_of(qk::launch_attn_paged(b, static_cast<int>(dim), dtype, static_cast<const uint8_t*>(pages), q, q_stride,
+                                         static_cast<int>(n_heads), scale, window, out, ws,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int qk_attn_prompt(int dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                   int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int64_t n_seq, int64_t n_q, int64_t n_k,
+                   int64_t n_heads, int64_t n_kv_heads, int64_t head_dim, float scale, int causal, int64_t window,
+                   void* out, void* stream) {
+  const int64_t es = float_bytes(dtype);
+  if (es == 0) return QK_E_TYPE;
+  if (!is_head_dim(head_dim) || !heads_ok(n_heads, n_kv_heads)) return QK_E_SHAPE;
+  const int64_t width = n_heads * head_dim, kv_width = n_kv_heads * head_dim;
+  if (n_seq < 0 || n_seq > INT32_MAX / 64 || n_q < 0 || n_q > kMaxRows || n_k < 0 || n_k > kMaxRows) return QK_E_SHAPE;
+  if (!std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0) return QK_E_ARG;
+  if (n_q == 0) return QK_OK;
+  if (cu_q == nullptr || cu_k == nullptr) return QK_E_NULL;
+  if (!aligned4(cu_q) || !aligned4(cu_k)) return QK_E_ALIGN;
+  int rc = QK_OK;
+  if ((rc = check_rows(q, q_stride, width, es)) != QK_OK) return rc;
+  if (n_k > 0) {
+    if ((rc = check_rows(k, k_stride, kv_width, es)) != QK_OK) return rc;
+    if ((rc = check_rows(v, v_stride, kv_width, es)) != QK_OK) return rc;
+  }
+  if ((rc = check_rows(out, width, width, es)) != QK_OK) return rc;
+  if (overlaps(q, q_stride, out, width, n_q, es)) return QK_E_ARG;
+  const qk::PromptBatch b{cu_q, cu_k, q_stride, k_stride, v_stride, n_q, n_k, window, static_cast<int>(n_seq),
+                          static_cast<int>(n_heads), static_cast<int>(n_kv_heads), causal};
+  return status_of(qk::launch_attn_prompt(b, static_cast<int>(head_dim), dtype, q, k, v, scale, out,
+                                          static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -7,7 +7,7 @@
 
 namespace qk {
 
-enum WType : int { kQ4_0 = 2, kQ4_1 = 3, kQ5_0 = 6, kQ5_1 = 7, kQ8_0 = 8, kQ8_1 = 9, kQ2_K = 10, kQ3_K = 11, kQ4_K = 12, kQ5_K = 13, kQ6_K = 14, kQ8_K = 15 };
+enum WType : int { kF32 = 0, kF16 = 1, kBF16 = 30, kQ4_0 = 2, kQ4_1 = 3, kQ5_0 = 6, kQ5_1 = 7, kQ8_0 = 8, kQ8_1 = 9, kQ2_K = 10, kQ3_K = 11, kQ4_K = 12, kQ5_K = 13, kQ6_K = 14, kQ8_K = 15 };
 
 // The work-items of one launch are counted in 32 bits (the dispatch packet's grid
 // size).  Launchers size their grids through launch_grid and refuse a larger launch
@@ -83,5 +83,21 @@ hipError_t launch_dequantize(int type, const uint8_t* src, float* dst, int64_t n
 bool read_probe_kb_ok(int kb);
 hipError_t launch_read_probe(const uint8_t* src, int64_t bytes, uint32_t* out, int kb, int64_t grid_blocks,
                              int nontemporal, hipStream_t s, hipEvent_t ev_start, hipEvent_t ev_stop);
+
+// The paged Q4_0 KV cache and attention (qk_kv.hip, qk_attn_paged.hip,
+// qk_attn_prompt.hip).  dtype is kF32, kF16 or kBF16, dim 64, 96, 128 or 256; n_rot 0 or a
+// multiple of 16; strides are in elements, multiples of 16 bytes.  q null: no query rows.
+struct KvBatch;      // qk_kv.h
+struct PromptBatch;  // qk_kv.h
+hipError_t launch_kv_append(const KvBatch& b, int dim, int dtype, uint8_t* pages, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const void* q, int64_t q_stride, int n_heads,
+                            const float* rope, int64_t rope_rows, int n_rot, int halves, void* q_out, hipStream_t s);
+hipError_t launch_kv_read(const KvBatch& b, int dim, int dtype, const uint8_t* pages, void* k_out, void* v_out,
+                          hipStream_t s);
+int64_t attn_paged_ws_bytes(const KvBatch& b, int dim, int n_heads);
+hipError_t launch_attn_paged(const KvBatch& b, int dim, int dtype, const uint8_t* pages, const void* q, int64_t q_stride,
+                             int n_heads, float scale, int64_t window, void* out, void* ws, hipStream_t s);
+hipError_t launch_attn_prompt(const PromptBatch& b, int dim, int dtype, const void* q, const void* k, const void* v,
+                              float scale, void* out, hipStream_t s);
 
 }  // namespace qk

@@ -1,0 +1,167 @@
+"""Host-side checks of the KV-cache and attention calls (no GPU): sizes, and the refusal of bad
+arguments before anything is enqueued.  Pointers are never dereferenced: every call below
+fails validation or has no rows.  The cache layout's plain forms are checked against each other."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import kv_reference as ref
+import quantized_gemv_quantize_amd as qk
+
+P = ctypes.c_void_p
+A, B_, C_, D_ = (P(0x10000000 * i) for i in (1, 2, 3, 4))  # aligned, far apart, never dereferenced
+OFF = P(0x10000008)
+OK, TYPE, SHAPE, ALIGN, NULL, LIMIT, ARG = 0, 1, 3, 4, 5, 7, 8
+F32, F16, BF16 = qk.QK_TYPE_F32, qk.QK_TYPE_F16, qk.QK_TYPE_BF16
+
+
+def batch(**kw):
+    d = dict(type=qk.QK_TYPE_Q4_0, page_tokens=32, n_pages=10, n_kv_heads=2, head_dim=128, page_table=0x1000, max_pages=4,
+             cu=0x2000, start=0x3000, n_seq=3, n_rows=5)
+    d.update(kw)
+    return qk._KVBatch(**d)
+
+
+BAD_BATCHES = [
+    (dict(type=qk.QK_TYPE_Q8_0), TYPE), (dict(type=99), TYPE), (dict(page_tokens=8), ARG), (dict(page_tokens=48), ARG),
+    (dict(page_tokens=512), ARG), (dict(head_dim=80), SHAPE), (dict(head_dim=0), SHAPE), (dict(head_dim=512), SHAPE),
+    (dict(n_kv_heads=0), SHAPE), (dict(n_kv_heads=1025), SHAPE), (dict(n_pages=-1), SHAPE), (dict(n_pages=2 ** 31), SHAPE),
+    (dict(max_pages=-1), SHAPE), (dict(max_pages=2 ** 31 // 32), SHAPE), (dict(n_seq=-1), SHAPE),
+    (dict(n_seq=2 ** 31), SHAPE), (dict(n_rows=-1), SHAPE), (dict(n_rows=2 ** 31), SHAPE), (dict(cu=0), NULL),
+    (dict(start=0), NULL), (dict(page_table=0), NULL), (dict(cu=0x2002), ALIGN), (dict(start=0x3001), ALIGN),
+    (dict(page_table=0x1002), ALIGN)]
+
+
+def append(b, pages=A, dtype=F32, k=B_, ks=256, v=B_, vs=256, q=C_, qs=1024, h=8, rope=B_, rows=100, rot=128, style=0,
+           q_out=D_):
+    return qk.lib().qk_kv_append(b, pages, dtype, k, ks, v, vs, q, qs, h, rope, rows, rot, style, q_out, None)
+
+
+def paged(b, pages=A, dtype=F32, q=C_, qs=1024, h=8, scale=0.1, window=0, out=D_, ws=A, ws_bytes=1 << 40):
+    return qk.lib().qk_attn_paged(b, pages, dtype, q, qs, h, scale, window, out, ws, ws_bytes, None)
+
+
+def read(b, pages=A, dtype=F32, k=C_, v=D_):
+    return qk.lib().qk_kv_read(b, pages, dtype, k, v, None)
+
+
+def prompt(dtype=F32, q=A, qs=1024, k=B_, ks=256, v=B_, vs=256, cu_q=P(0x1000), cu_k=P(0x1000), n_seq=2, n_q=9, n_k=9, h=8,
+           hk=2, dim=128, scale=0.1, causal=1, window=0, out=D_):
+    return qk.lib().qk_attn_prompt(dtype, q, qs, k, ks, v, vs, cu_q, cu_k, n_seq, n_q, n_k, h, hk, dim, scale, causal,
+                                   window, out, None)
+
+
+@pytest.mark.parametrize("kw,status", BAD_BATCHES)
+def test_batches_are_checked_by_every_call(kw, status):
+    for f in (append, read, paged):
+        assert f(batch(**kw)) == status, f.__name__
+    if status not in (NULL, ALIGN):
+        assert qk.lib().qk_attn_paged_ws_bytes(batch(**kw), 8) == 0
+
+
+def test_null_batch_and_no_rows():
+    for f in (append, read, paged):
+        assert f(None) == NULL
+        assert f(batch(n_rows=0, cu=0, start=0, page_table=0), pages=None) == OK
+    assert prompt(n_q=0, q=None, k=None, v=None, cu_q=None, cu_k=None, out=None) == OK
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=qk.QK_TYPE_Q8_0), TYPE), (dict(dtype=2), TYPE), (dict(style=2), ARG), (dict(style=-1), ARG),
+    (dict(rot=130), SHAPE), (dict(rot=8), SHAPE), (dict(rot=-16), SHAPE), (dict(rot=144), SHAPE), (dict(rows=-1), SHAPE),
+    (dict(h=0), SHAPE), (dict(h=7), SHAPE), (dict(h=2 ** 62), SHAPE), (dict(ks=255), SHAPE), (dict(vs=128), SHAPE),
+    (dict(qs=1023), SHAPE), (dict(ks=2 ** 40), SHAPE), (dict(pages=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL),
+    (dict(q_out=None), NULL), (dict(rope=None), NULL), (dict(pages=OFF), ALIGN), (dict(k=OFF), ALIGN), (dict(v=OFF), ALIGN),
+    (dict(q=OFF), ALIGN), (dict(q_out=OFF), ALIGN), (dict(rope=OFF), ALIGN), (dict(ks=257), ALIGN),
+    (dict(dtype=F16, vs=260), ALIGN), (dict(q_out=C_), ARG), (dict(q_out=P(C_.value + 16)), ARG)])
+def test_append_refusals(kw, status):
+    assert append(batch(), **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=8), TYPE), (dict(pages=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(pages=OFF), ALIGN),
+    (dict(k=OFF), ALIGN), (dict(v=OFF), ALIGN)])
+def test_read_refusals(kw, status):
+    assert read(batch(), **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=qk.QK_TYPE_Q4_0), TYPE), (dict(h=0), SHAPE), (dict(h=9), SHAPE), (dict(h=2 ** 61), SHAPE),
+    (dict(h=1026), SHAPE), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG), (dict(window=-1), ARG),
+    (dict(qs=1000), SHAPE), (dict(qs=1026), ALIGN), (dict(q=None), NULL), (dict(out=None), NULL), (dict(pages=None), NULL),
+    (dict(q=OFF), ALIGN), (dict(out=OFF), ALIGN), (dict(out=C_), ARG)])
+def test_paged_refusals(kw, status):
+    assert paged(batch(), **kw) == status
+
+
+def test_paged_workspace_is_checked():
+    """Where a workspace is needed, too small, missing or misaligned ones are refused."""
+    b = batch(max_pages=4096, n_pages=100000)
+    need = qk.lib().qk_attn_paged_ws_bytes(b, 8)
+    assert need >= 0
+    if need:
+        assert paged(b, ws_bytes=need - 1) == ARG
+        assert paged(b, ws=None) == NULL
+        assert paged(b, ws=OFF) == ALIGN
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=7), TYPE), (dict(dim=72), SHAPE), (dict(h=7), SHAPE), (dict(h=0), SHAPE), (dict(hk=0), SHAPE),
+    (dict(hk=-2), SHAPE), (dict(h=2 ** 62, hk=2), SHAPE), (dict(n_seq=-1), SHAPE), (dict(n_q=-1), SHAPE), (dict(n_k=-1), SHAPE),
+    (dict(n_q=2 ** 31), SHAPE), (dict(n_k=2 ** 31), SHAPE), (dict(scale=float("-inf")), ARG), (dict(causal=2), ARG),
+    (dict(window=-5), ARG), (dict(cu_q=None), NULL), (dict(cu_k=None), NULL), (dict(cu_q=P(0x1002)), ALIGN), (dict(qs=8), SHAPE),
+    (dict(ks=255), SHAPE), (dict(vs=0), SHAPE), (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL),
+    (dict(out=None), NULL), (dict(q=OFF), ALIGN), (dict(k=OFF), ALIGN), (dict(v=OFF), ALIGN), (dict(out=OFF), ALIGN),
+    (dict(ks=258), ALIGN), (dict(dtype=BF16, ks=260), ALIGN), (dict(out=A), ARG)])
+def test_prompt_refusals(kw, status):
+    assert prompt(**kw) == status
+
+
+def test_page_bytes():
+    for tokens in (16, 32, 64, 128, 256):
+        for dim in (64, 96, 128, 256):
+            assert qk.qk_kv_page_bytes(qk.QK_TYPE_Q4_0, tokens, dim) == ref.page_bytes(tokens, dim)
+            # as many bytes as the Q4_0 blocks of the same values
+            assert ref.page_bytes(tokens, dim) == 2 * tokens * qk.qk_row_bytes(qk.QK_TYPE_Q4_0, dim)
+    for bad in ((qk.QK_TYPE_Q8_0, 32, 128), (qk.QK_TYPE_Q4_0, 8, 128), (qk.QK_TYPE_Q4_0, 32, 100)):
+        assert qk.qk_kv_page_bytes(*bad) == 0
+    # the float types are no block types
+    assert all(qk.qk_block_elems(t) == 0 and qk.qk_row_bytes(t, 256) == 0 for t in (F32, F16, BF16))
+
+
+def test_binding_checks_its_tensors():
+    import torch
+    pages = torch.zeros(4, 2, ref.page_bytes(16, 64), dtype=torch.uint8)
+    table, cu, start = (torch.zeros(s, dtype=torch.int32) for s in ((3, 2), (4,), (3,)))
+    k = torch.zeros(5, 2, 64)
+    with pytest.raises(TypeError):
+        qk.qk_kv_append(pages, 16, table, cu, start, k, k.half())
+    with pytest.raises(TypeError):
+        qk.qk_kv_append(pages, 16, table, cu, start, k.double(), k.double())
+    with pytest.raises(ValueError):
+        qk.qk_kv_append(pages, 32, table, cu, start, k, k)
+    with pytest.raises(ValueError):
+        qk.qk_kv_append(pages, 16, table.long(), cu, start, k, k)
+    with pytest.raises(ValueError):
+        qk.qk_kv_append(pages, 16, table, cu[:3], start, k, k)
+    with pytest.raises(ValueError):
+        qk.qk_kv_append(pages, 16, table, cu, start, k.transpose(1, 2), k.transpose(1, 2))
+    with pytest.raises(ValueError):
+        qk.qk_attn_paged(pages, 16, table, cu, start, k, out=torch.zeros(5, 2, 32))
+    with pytest.raises(ValueError):
+        qk.qk_attn_prompt(k, k[:4], k[:4], cu)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_layout_forms_agree(dim):
+    rng = np.random.default_rng(dim)
+    pages = rng.integers(0, 256, (2, 3, ref.page_bytes(16, dim)), dtype=np.uint8)
+    half = 16 * (dim // 2 + dim // 16)
+    for base in (8 * dim, half + 8 * dim):
+        sc = rng.uniform(-1, 1, (2, 3, dim // 2)).astype(np.float16)
+        pages[:, :, base:base + dim] = sc.view(np.uint8).reshape(2, 3, dim)
+    for is_v, a in enumerate(ref.unpack_pages(pages, 16, dim)):
+        for slot in (0, 7, 15):
+            codes, sc = ref.unpack_row(pages[1, 2], 16, dim, slot, bool(is_v))
+            assert np.array_equal(a[1, 2, slot], (codes - 8) * np.repeat(sc.astype(np.float64), 32))

@@ -1,0 +1,598 @@
+"""GPU tests of qk_kv_append, qk_kv_read, qk_attn_paged and qk_attn_prompt against plain
+64-bit forms (kv_reference.py states the tolerances' derivation).
+
+Codes, scales and read-back values have one right answer and are compared bit for bit.
+"""
+import numpy as np
+import pytest
+
+import kv_reference as ref
+import quantized_gemv_quantize_amd as qk
+from oracle import oracle as orc
+
+pytestmark = pytest.mark.gpu
+
+DIMS = [64, 96, 128, 256]
+TYPES = ["f32", "f16", "bf16"]
+
+
+@pytest.fixture(scope="module")
+def torch_cuda():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a visible MI355X"
+    qk.lib()
+    return torch
+
+
+def say(*a):
+    print("[case]", *a, flush=True)
+
+
+def dt(torch, name):
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[name]
+
+
+def typed(torch, a, name):
+    """(device tensor of the type, the same values as f64)."""
+    t = torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(dt(torch, name))
+    return t.cuda(), t.double().numpy()
+
+
+def i32(torch, a):
+    return torch.from_numpy(np.asarray(a, np.int32)).cuda()
+
+
+class Cache:
+    """A cache of random codes and scales with a shuffled page table, on both sides."""
+
+    def __init__(self, torch, rng, lens, hk, dim, page, spare=3, fill=None):
+        self.page, self.dim, self.hk = page, dim, hk
+        need = [-(-n // page) for n in lens]
+        n_pages = sum(need) + spare
+        half = page * (dim // 2 + dim // 16)
+        raw = rng.integers(0, 256, (n_pages, hk, 2 * half), dtype=np.uint8)
+        for base in (0, half):
+            n = half - page * dim // 2
+            sc = (rng.uniform(0.1, 0.4, (n_pages, hk, n // 2)) * rng.choice([-1, 1], (n_pages, hk, n // 2)))
+            raw[:, :, base + page * dim // 2:base + half] = sc.astype(np.float16).view(np.uint8).reshape(n_pages, hk, n)
+        if fill is not None:
+            raw[:] = fill
+        order = rng.permutation(n_pages)
+        table = np.full((len(lens), max(need + [0]) + 1), -1, np.int32)
+        at = 0
+        for i, m in enumerate(need):
+            table[i, :m] = order[at:at + m]
+            at += m
+        self.raw, self.table = raw, table
+        self.pages, self.dtable = torch.from_numpy(raw).cuda(), i32(torch, table)
+
+    def values(self):
+        return ref.unpack_pages(self.raw, self.page, self.dim)
+
+
+# ---------------------------------------------------------------------------
+# append and read
+
+def _append_case(torch, rng, dtype, dim, hk, h, page, new, start, style, n_rot, strided=False):
+    n = sum(new)
+    c = Cache(torch, rng, [a + b for a, b in zip(new, start)], hk, dim, page)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    x = rng.standard_normal((n, h + 2 * hk, dim)) * np.exp(rng.standard_normal((n, h + 2 * hk, 1)))
+    t, f = typed(torch, x, dtype)
+    tq, tk, tv = t[:, :h], t[:, h:h + hk], t[:, h + hk:]
+    if not strided:
+        tq, tk, tv = tq.contiguous(), tk.contiguous(), tv.contiguous()
+    f = f.astype(np.float32)
+    fq, fk, fv = f[:, :h], f[:, h:h + hk], f[:, h + hk:]
+    rows = max(a + b for a, b in zip(new, start))
+    rope = ref.rope_table(rows, n_rot) if n_rot else None
+    drope = torch.from_numpy(rope).cuda() if n_rot else None
+    got_q = qk.qk_kv_append(c.pages, page, c.dtable, i32(torch, cu), i32(torch, start), tk, tv, q=tq, rope=drope,
+                            rope_style=qk.QK_ROPE_HALVES if style == "halves" else qk.QK_ROPE_PAIRS)
+    pos = np.concatenate([s + np.arange(m) for s, m in zip(start, new)])
+    seq = np.repeat(np.arange(len(new)), new)
+    if n_rot:
+        fq, fk = (ref.rotate(a, rope[pos], style) for a in (fq, fk))
+    want = c.raw.copy()
+    for is_v, a in ((False, fk), (True, fv)):
+        blocks = orc.quantize(orc.Q4_0, a.reshape(-1, dim)).reshape(n, hk, dim // 32, 18)
+        for r in range(n):
+            p, slot = c.table[seq[r], pos[r] // page], pos[r] % page
+            base = page * (dim // 2 + dim // 16) if is_v else 0
+            for head in range(hk):
+                for b in range(dim // 32):
+                    d, qs = blocks[r, head, b, :2], blocks[r, head, b, 2:]
+                    code = np.concatenate([qs & 15, qs >> 4])
+                    for g in range(4):
+                        w = sum(int(code[8 * g + j]) << (4 * (j // 2 + 4 * (j % 2))) for j in range(8))
+                        o = base + slot * dim // 2 + (g * (dim // 32) + b) * 4
+                        want[p, head, o:o + 4] = np.frombuffer(np.uint32(w).tobytes(), np.uint8)
+                    o = base + page * dim // 2 + (slot * (dim // 32) + b) * 2
+                    want[p, head, o:o + 2] = d
+    torch.cuda.synchronize()
+    got = c.pages.cpu().numpy()
+    assert np.array_equal(got, want), f"{int((got != want).sum())} cache bytes differ"
+    wq = torch.from_numpy(fq).to(dt(torch, dtype))
+    assert torch.equal(got_q.cpu().view(torch.uint8), wq.contiguous().view(torch.uint8)), "rotated queries differ"
+    # and back: every value exact in f32, rounded once
+    ko, vo = qk.qk_kv_read(c.pages, page, c.dtable, i32(torch, cu), i32(torch, start), n, dim, dtype=dt(torch, dtype))
+    kv = ref.unpack_pages(want, page, dim)
+    for o, a in zip((ko, vo), kv):
+        w = np.stack([a[c.table[s, p // page], :, p % page] for s, p in zip(seq, pos)])
+        assert torch.equal(o.cpu(), torch.from_numpy(w.astype(np.float32)).to(dt(torch, dtype)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+def test_append_and_read_bit_exact(torch_cuda, dtype, dim):
+    rng = np.random.default_rng(100 + dim)
+    for hk, h, page, new, start, style, n_rot in (
+            (1, 1, 16, [1], [0], "halves", dim), (2, 6, 32, [3, 0, 5, 1], [15, 7, 0, 300], "pairs", dim),
+            (3, 3, 64, [17, 2], [62, 4], "halves", dim // 2), (2, 2, 256, [5], [254], "pairs", 16),
+            (8, 8, 128, [2, 1], [0, 1], "halves", 0)):
+        say("append", dtype, dim, hk, h, page, new, start, style, n_rot)
+        _append_case(torch_cuda, rng, dtype, dim, hk, h, page, new, start, style, n_rot, strided=hk == 2)
+
+
+def test_append_many_sequences(torch_cuda):
+    """More sequences than a wavefront has lanes; empty ones among them."""
+    rng = np.random.default_rng(5)
+    new = list(rng.integers(0, 3, 150))
+    _append_case(torch_cuda, rng, "f32", 64, 1, 2, 16, new, list(rng.integers(0, 60, 150)), "halves", 64)
+
+
+def test_append_block_rule_edges(torch_cuda):
+    """Ties, signed zeros, constant and tiny blocks: the codes are qk_quantize_row's."""
+    torch = torch_cuda
+    rows = [np.zeros(32), np.full(32, -3.25), np.r_[2.0, -2.0, np.zeros(30)], np.r_[np.zeros(30), -2.0, 2.0],
+            np.r_[np.zeros(7), -1.5, 1.5, np.zeros(23)], np.full(32, 1e-42), np.full(32, 3e5), np.arange(32) - 16.0,
+            np.r_[-0.0, np.zeros(31)], np.linspace(-1, 1, 32), np.r_[1e-39, np.full(31, -1e-39)], np.full(32, 5e-7)]
+    x = np.concatenate(rows * 2).astype(np.float32).reshape(-1, 1, 64)
+    n = x.shape[0]
+    c = Cache(torch, np.random.default_rng(0), [n], 1, 64, 16)
+    t = torch.from_numpy(x).cuda()
+    qk.qk_kv_append(c.pages, 16, c.dtable, i32(torch, [0, n]), i32(torch, [0]), t, t)
+    blocks = qk.qk_quantize_row(qk.QK_TYPE_Q4_0, t.reshape(-1)).cpu().numpy().reshape(n, 2, 18)
+    got = c.pages.cpu().numpy()
+    for r in range(n):
+        for is_v in (False, True):
+            codes, sc = ref.unpack_row(got[c.table[0, r // 16], 0], 16, 64, r % 16, is_v)
+            for b in range(2):
+                qs = blocks[r, b, 2:]
+                assert np.array_equal(codes[32 * b:32 * b + 32], np.concatenate([qs & 15, qs >> 4])), (r, b)
+                assert sc[b:b + 1].tobytes() == blocks[r, b, :2].tobytes(), (r, b)
+
+
+def test_rows_without_a_place_are_left_alone(torch_cuda):
+    """Bad page entries, positions beyond the table or the rope rows, rows behind the last sequence."""
+    torch = torch_cuda
+    rng = np.random.default_rng(9)
+    hk, h, dim, page = 2, 4, 64, 16
+    c = Cache(torch, rng, [40, 40, 40, 40], hk, dim, page)
+    c.table[0, 2], c.table[1, 1] = c.raw.shape[0], -7
+    c.dtable.copy_(torch.from_numpy(c.table))
+    start = [30, 14, -3, c.table.shape[1] * page - 2]
+    cu = [0, 4, 8, 12, 16]
+    n = 20  # rows 16..19 behind the last sequence
+    x = rng.standard_normal((n, hk, dim)).astype(np.float32)
+    t = torch.from_numpy(x).cuda()
+    q = torch.from_numpy(rng.standard_normal((n, h, dim)).astype(np.float32)).cuda()
+    rope = torch.from_numpy(ref.rope_table(60, dim)).cuda()
+    q_out = torch.full((n, h, dim), 77.0, device="cuda")
+    qk.qk_kv_append(c.pages, page, c.dtable, i32(torch, cu), i32(torch, start), t, t, q=q, rope=rope, q_out=q_out)
+    got, qo = c.pages.cpu().numpy(), q_out.cpu().numpy()
+    pos = [s + i for s in start for i in range(4)]
+    written = set()
+    for r, p in enumerate(pos):
+        s = r // 4
+        ok = 0 <= p // page < c.table.shape[1] and 0 <= c.table[s, p // page] < c.raw.shape[0]
+        assert (qo[r] != 77.0).all() == (0 <= p < 60) and (qo[r] == 77.0).all() == (not 0 <= p < 60), r
+        if ok and p < 60:
+            written.add((int(c.table[s, p // page]), p % page))
+    assert (qo[16:] == 77.0).all()
+    k0, k1 = (ref.unpack_pages(a, page, dim)[0] for a in (c.raw, got))
+    for pg in range(c.raw.shape[0]):
+        for slot in range(page):
+            same = np.array_equal(k0[pg, :, slot], k1[pg, :, slot])
+            assert same == ((pg, slot) not in written), (pg, slot)
+    # reading the same rows: zeros where there is no page, nothing behind the last sequence
+    ko, vo = (torch.full((n, hk, dim), 55.0, device="cuda") for _ in range(2))
+    qk.qk_kv_read(c.pages, page, c.dtable, i32(torch, cu), i32(torch, start), n, dim, k_out=ko, v_out=vo)
+    ko = ko.cpu().numpy()
+    assert (ko[16:] == 55.0).all()
+    for r, p in enumerate(pos):
+        s = r // 4
+        ok = p >= 0 and p // page < c.table.shape[1] and 0 <= c.table[s, p // page] < c.raw.shape[0]
+        want = k1[c.table[s, p // page], :, p % page].astype(np.float32) if ok else np.zeros((hk, dim), np.float32)
+        assert np.array_equal(ko[r], want), r
+    # and attending from them: a row sees its valid pages only, none at all gives zeros
+    out = torch.full((n, h, dim), 33.0, device="cuda")
+    qk.qk_attn_paged(c.pages, page, c.dtable, i32(torch, cu), i32(torch, start), q, out=out)
+    o, qn = out.cpu().numpy().astype(np.float64), q.cpu().numpy().astype(np.float64)
+    assert (o[16:] == 33.0).all()
+    kk, vv = ref.unpack_pages(got, page, dim)
+    for r, p in enumerate(pos):
+        s = r // 4
+        t_ok = [u for u in range(0, max(p + 1, 0)) if u // page < c.table.shape[1]
+                and 0 <= c.table[s, u // page] < c.raw.shape[0]]
+        for head in range(h):
+            k, v = (np.array([a[c.table[s, u // page], head // 2, u % page] for u in t_ok]).reshape(-1, dim)
+                    for a in (kk, vv))
+            w, av, size = ref.attend(qn[r:r + 1, head], k, v, dim ** -0.5, np.ones((1, len(t_ok)), bool))
+            assert np.all(np.abs(o[r, head] - w[0]) <= ref.tolerance("f32", w, av, size, 64, dim)[0]), (r, head)
+            if not t_ok:
+                assert (o[r, head] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# attention over the cache
+
+def _paged_want(c, q, new, start, scale, window):
+    k, v = c.values()
+    n, h, dim = q.shape
+    out, absv, size = np.zeros((n, h, dim)), np.zeros((n, h, dim)), np.zeros((n, h))
+    at = 0
+    for i, (m, s) in enumerate(zip(new, start)):
+        t = s + m
+        if m == 0:
+            continue
+        p = np.arange(t)
+        ks, vs = (a[c.table[i, p // c.page], :, p % c.page] for a in (k, v))
+        here = s + np.arange(m)[:, None]
+        seen = p <= here
+        if window:
+            seen = seen & (p > here - window)
+        for j in range(h):
+            g = j // (h // c.hk)
+            out[at:at + m, j], absv[at:at + m, j], size[at:at + m, j] = ref.attend(q[at:at + m, j], ks[:, g], vs[:, g],
+                                                                                   scale, seen)
+        at += m
+    return out, absv, size
+
+
+def _check(dtype, got, want, absv, size, n, dim):
+    g = got.double().cpu().numpy()
+    tol = ref.tolerance(dtype, want.reshape(-1, dim), absv.reshape(-1, dim), size.reshape(-1), n, dim).reshape(want.shape)
+    err = np.abs(g - want)
+    bad = ~(err <= tol)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} outputs off, worst {np.nanmax(err / tol):.3g} of the bound"
+
+
+def _paged_case(torch, seed, dtype, dim, hk, h, page, new, start, window=0, scale=None, strided=False, q_size=1.5):
+    rng = np.random.default_rng(seed)
+    say("paged", dtype, dim, hk, h, page, new, start, window)
+    c = Cache(torch, rng, [a + b for a, b in zip(new, start)], hk, dim, page)
+    n = sum(new)
+    tq, fq = typed(torch, rng.standard_normal((n, h + (2 if strided else 0), dim)) * q_size, dtype)
+    tq, fq = tq[:, :h], fq[:, :h]
+    scale = dim ** -0.5 if scale is None else scale
+    got = qk.qk_attn_paged(c.pages, page, c.dtable, i32(torch, np.concatenate([[0], np.cumsum(new)])), i32(torch, start), tq,
+                           scale=scale, window=window)
+    _check(dtype, got, *_paged_want(c, fq, new, start, np.float64(np.float32(scale)), window),
+           max([a + b for a, b in zip(new, start)]), dim)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+def test_paged_lengths(torch_cuda, dtype, dim):
+    """From one token on, at and around the tiles' and pages' ends."""
+    start = [0, 1, 14, 15, 16, 30, 31, 32, 33, 62, 63, 64, 127, 128, 200, 511]
+    _paged_case(torch_cuda, 1, dtype, dim, 2, 4, 16, [1] * len(start), start)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hk,h", [(1, 1), (1, 5), (2, 32), (4, 12), (1, 16), (1, 17), (8, 8), (1, 40)])
+def test_paged_groups_and_rows(torch_cuda, dtype, hk, h):
+    """Every way the rows of a group fill the matrix tiles, with several new rows per sequence."""
+    _paged_case(torch_cuda, 2, dtype, 64, hk, h, 32, [3, 1, 0, 7, 20], [40, 0, 9, 100, 13])
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_paged_page_sizes(torch_cuda, page):
+    _paged_case(torch_cuda, 3, "f16", 128, 2, 8, page, [1, 4, 2], [700, 333, 1022], strided=True)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("window", [1, 2, 16, 17, 100, 5000])
+def test_paged_window(torch_cuda, dtype, window):
+    _paged_case(torch_cuda, 4, dtype, 96, 2, 6, 16, [3, 1, 5], [130, 0, 1001], window=window)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_paged_long(torch_cuda, dtype, dim):
+    """Long enough for the split over the cache, beside short ones."""
+    _paged_case(torch_cuda, 5, dtype, dim, 1, 4, 64, [1, 1, 2], [20011, 0, 3])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_paged_peaked_and_flat(torch_cuda, dtype):
+    """Scores far apart (one weight of almost 1), all equal (scale 0), and a negative scale."""
+    _paged_case(torch_cuda, 6, dtype, 128, 2, 4, 32, [2, 1], [300, 77], q_size=30.0)
+    _paged_case(torch_cuda, 7, dtype, 128, 2, 4, 32, [2, 1], [300, 77], scale=0.0)
+    _paged_case(torch_cuda, 8, dtype, 128, 2, 4, 32, [2, 1], [300, 77], scale=-0.2)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_paged_query_range(torch_cuda, dtype):
+    """Queries far from 1: large, tiny and zero rows."""
+    torch = torch_cuda
+    rng = np.random.default_rng(77)
+    c = Cache(torch, rng, [100], 1, 64, 16)
+    x = rng.standard_normal((6, 2, 64)) * np.array([1e4, 3e-5, 0.0, 1.0, 1e-3, 100.0])[:, None, None]
+    tq, fq = typed(torch, x, dtype)
+    got = qk.qk_attn_paged(c.pages, 16, c.dtable, i32(torch, [0, 6]), i32(torch, [94]), tq, scale=2.0 ** -10)
+    _check(dtype, got, *_paged_want(c, fq, [6], [94], 2.0 ** -10, 0), 100, 64)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_paged_value_scales(torch_cuda, dtype):
+    """Value scales over the f16 range, from subnormal to the largest, in one row."""
+    torch = torch_cuda
+    rng = np.random.default_rng(78)
+    dim, page = 128, 16
+    c = Cache(torch, rng, [150], 1, dim, page)
+    half = page * (dim // 2 + dim // 16)
+    sc = c.raw[:, :, half + page * dim // 2:].copy().view(np.float16)
+    sc[:] = (2.0 ** rng.uniform(-24, 12, sc.shape)).astype(np.float16)
+    c.raw[:, :, half + page * dim // 2:] = sc.view(np.uint8)
+    c.pages.copy_(torch.from_numpy(c.raw))
+    tq, fq = typed(torch, rng.standard_normal((3, 2, dim)), dtype)
+    got = qk.qk_attn_paged(c.pages, page, c.dtable, i32(torch, [0, 3]), i32(torch, [147]), tq)
+    _check(dtype, got, *_paged_want(c, fq, [3], [147], np.float64(np.float32(dim ** -0.5)), 0), 150, dim)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_paged_garbage_in_masked_places(torch_cuda, dtype):
+    """Slots behind the last position and pages no row may see hold infinities and NaN."""
+    torch = torch_cuda
+    rng = np.random.default_rng(10)
+    dim, page, new, start = 64, 64, [2, 1], [70, 20]
+    c = Cache(torch, rng, [72, 21], 2, dim, page)
+    raw = np.full_like(c.raw, 0xFF)  # every f16 scale a NaN
+    half = page * (dim // 2 + dim // 16)
+    for i, t in enumerate([72, 21]):
+        for p in range(t):
+            pg, s = c.table[i, p // page], p % page
+            for base in (0, half):
+                a = base + s * dim // 2
+                raw[pg, :, a:a + dim // 2] = c.raw[pg, :, a:a + dim // 2]
+                a = base + page * dim // 2 + s * dim // 16
+                raw[pg, :, a:a + dim // 16] = c.raw[pg, :, a:a + dim // 16]
+    c.raw = raw
+    c.pages.copy_(torch.from_numpy(raw))
+    tq, fq = typed(torch, rng.standard_normal((3, 4, dim)), dtype)
+    for window in (0, 9):
+        got = qk.qk_attn_paged(c.pages, page, c.dtable, i32(torch, [0, 2, 3]), i32(torch, start), tq, window=window)
+        _check(dtype, got, *_paged_want(c, fq, new, start, np.float64(np.float32(dim ** -0.5)), window), 72, dim)
+
+
+def test_paged_offsets_past_32_bits(torch_cuda):
+    """A cache of more than 4 GiB whose last pages are in use."""
+    torch = torch_cuda
+    rng = np.random.default_rng(11)
+    dim, page, hk = 128, 256, 8
+    c = Cache(torch, rng, [500], hk, dim, page)
+    n_pages = 2 ** 32 // (hk * ref.page_bytes(page, dim)) + 8
+    big = torch.empty((n_pages, hk, ref.page_bytes(page, dim)), dtype=torch.uint8, device="cuda")
+    first = n_pages - c.raw.shape[0]
+    big[first:] = c.pages
+    table = torch.where(c.dtable >= 0, c.dtable + first, c.dtable)
+    tq, fq = typed(torch, rng.standard_normal((2, 8, dim)), "f16")
+    cu, start = i32(torch, [0, 2]), i32(torch, [498])
+    got = qk.qk_attn_paged(big, page, table, cu, start, tq)
+    _check("f16", got, *_paged_want(c, fq, [2], [498], np.float64(np.float32(dim ** -0.5)), 0), 500, dim)
+    a, b = qk.qk_kv_read(big, page, table, cu, start, 2, dim), qk.qk_kv_read(c.pages, page, c.dtable, cu, start, 2, dim)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    t = torch.randn(2, hk, dim, device="cuda")
+    qk.qk_kv_append(big, page, table, cu, start, t, t)
+    qk.qk_kv_append(c.pages, page, c.dtable, cu, start, t, t)
+    assert torch.equal(big[first:], c.pages)
+
+
+def test_paged_is_deterministic_and_reuses_a_workspace(torch_cuda):
+    torch = torch_cuda
+    rng = np.random.default_rng(12)
+    c = Cache(torch, rng, [9000, 40], 2, 128, 64)
+    tq, _ = typed(torch, rng.standard_normal((2, 8, 128)), "f32")
+    cu, start = i32(torch, [0, 1, 2]), i32(torch, [8999, 39])
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")  # NaN wherever it is read as f32
+    first = qk.qk_attn_paged(c.pages, 64, c.dtable, cu, start, tq, ws=ws)
+    for _ in range(3):
+        assert torch.equal(first, qk.qk_attn_paged(c.pages, 64, c.dtable, cu, start, tq, ws=ws))
+        assert torch.equal(first, qk.qk_attn_paged(c.pages, 64, c.dtable, cu, start, tq))
+
+
+def test_calls_on_another_stream_and_in_a_graph(torch_cuda):
+    """A decode step on a side stream, then captured once and replayed while start moves on."""
+    torch = torch_cuda
+    rng = np.random.default_rng(13)
+    dim, hk, h, page = 128, 2, 8, 32
+    c = Cache(torch, rng, [400, 90], hk, dim, page)
+    k, v, q = (torch.randn(2, n, dim, device="cuda") for n in (hk, hk, h))
+    rope = torch.from_numpy(ref.rope_table(500, dim)).cuda()
+    cu, start = i32(torch, [0, 1, 2]), i32(torch, [300, 50])
+
+    def step(pages, stream=None):
+        qr = qk.qk_kv_append(pages, page, c.dtable, cu, start, k, v, q=q, rope=rope, stream=stream)
+        return qk.qk_attn_paged(pages, page, c.dtable, cu, start, qr, stream=stream)
+
+    want = step(c.pages.clone())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step(c.pages.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(want, other)
+    pages = c.pages.clone()
+    with torch.cuda.stream(side):
+        step(pages.clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(pages)
+    eager = c.pages.clone()
+    for i in range(4):
+        start.copy_(torch.tensor([300 + i, 50 + i], dtype=torch.int32))
+        q.normal_()
+        k.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, step(eager)), i
+        assert torch.equal(pages, eager), i
+
+
+# ---------------------------------------------------------------------------
+# attention over prompts
+
+def _prompt_want(q, k, v, cu_q, cu_k, scale, causal, window):
+    n, h, dim = q.shape
+    g = h // k.shape[1]
+    out, absv, size = np.zeros((n, h, dim)), np.zeros((n, h, dim)), np.zeros((n, h))
+    for i in range(len(cu_q) - 1):
+        a, b, c, d = cu_q[i], cu_q[i + 1], cu_k[i], cu_k[i + 1]
+        here = (np.arange(b - a) + (d - c) - (b - a))[:, None]
+        p = np.arange(d - c)
+        seen = np.ones((b - a, d - c), bool)
+        if causal:
+            seen &= p <= here
+        if window:
+            seen &= p > here - window
+        for j in range(h):
+            out[a:b, j], absv[a:b, j], size[a:b, j] = ref.attend(q[a:b, j], k[c:d, j // g], v[c:d, j // g], scale, seen)
+    return out, absv, size
+
+
+def _prompt_case(torch, seed, dtype, dim, hk, h, lens, klens=None, causal=True, window=0, scale=None, strided=False,
+                 size=1.2):
+    rng = np.random.default_rng(seed)
+    say("prompt", dtype, dim, hk, h, lens, klens, causal, window)
+    cu_q = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    cu_k = cu_q if klens is None else np.concatenate([[0], np.cumsum(klens)]).astype(np.int32)
+    scale = dim ** -0.5 if scale is None else scale
+    if strided:  # q, k, v slices of one projection's rows
+        t, f = typed(torch, rng.standard_normal((cu_q[-1], h + 2 * hk, dim)) * size, dtype)
+        (tq, tk, tv), (fq, fk, fv) = ((x[:, :h], x[:, h:h + hk], x[:, h + hk:]) for x in (t, f))
+    else:
+        tq, fq = typed(torch, rng.standard_normal((cu_q[-1], h, dim)) * size, dtype)
+        (tk, fk), (tv, fv) = (typed(torch, rng.standard_normal((cu_k[-1], hk, dim)) * size, dtype) for _ in range(2))
+    got = qk.qk_attn_prompt(tq, tk, tv, i32(torch, cu_q), None if klens is None else i32(torch, cu_k), scale=scale,
+                            causal=causal, window=window)
+    want, absv, s = _prompt_want(fq, fk, fv, cu_q, cu_k, np.float64(np.float32(scale)), causal, window)
+    longest = int(np.diff(cu_k).max()) if len(cu_k) > 1 else 0
+    _check(dtype, got, want, absv, s, longest, dim)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+def test_prompt_lengths(torch_cuda, dtype, dim):
+    _prompt_case(torch_cuda, 20, dtype, dim, 2, 4, [1, 2, 0, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 200, 257])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hk,h", [(1, 1), (1, 5), (2, 32), (4, 12), (8, 8), (3, 3)])
+def test_prompt_groups_strided(torch_cuda, dtype, hk, h):
+    _prompt_case(torch_cuda, 21, dtype, 64, hk, h, [70, 1, 130, 0], strided=True)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [0, 1, 16, 65, 300])
+def test_prompt_masks(torch_cuda, dtype, causal, window):
+    _prompt_case(torch_cuda, 22, dtype, 128, 2, 6, [150, 7, 301], causal=causal, window=window)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_chunks_and_empty_rows(torch_cuda, dtype, dim, causal):
+    """More keys than rows (a chunk behind its prefix), fewer (rows that see nothing), and none."""
+    _prompt_case(torch_cuda, 23, dtype, dim, 1, 3, [40, 100, 9, 130, 1], [200, 37, 0, 259, 70], causal=causal)
+    _prompt_case(torch_cuda, 24, dtype, dim, 1, 3, [40, 100, 9], [200, 37, 0], causal=causal, window=20)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_prompt_long(torch_cuda, dtype):
+    _prompt_case(torch_cuda, 25, dtype, 64, 1, 1, [1500, 700])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_prompt_peaked_and_flat(torch_cuda, dtype):
+    _prompt_case(torch_cuda, 26, dtype, 128, 1, 2, [200], size=4.0)
+    _prompt_case(torch_cuda, 27, dtype, 128, 1, 2, [200], scale=0.0)
+    _prompt_case(torch_cuda, 28, dtype, 96, 1, 2, [200], scale=-0.3)
+
+
+def test_prompt_many_sequences(torch_cuda):
+    rng = np.random.default_rng(29)
+    _prompt_case(torch_cuda, 29, "bf16", 64, 1, 2, list(rng.integers(0, 40, 140)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_prompt_garbage_in_masked_places(torch_cuda, dtype):
+    """NaN and infinities in keys and values no row may see: behind a causal row, in the
+    next sequence, behind the last one."""
+    torch = torch_cuda
+    rng = np.random.default_rng(30)
+    dim, cu = 64, [0, 70, 100]
+    x = [rng.standard_normal((120, 2, dim)) for _ in range(3)]
+    (tq, fq), (tk, fk), (tv, fv) = (typed(torch, a, dtype) for a in x)
+    want = _prompt_want(fq[:100], fk, fv, cu, cu, np.float64(np.float32(dim ** -0.5)), True, 0)
+    for t, bad in ((tk, float("nan")), (tv, float("inf"))):
+        t[100:] = bad  # behind every sequence
+        t[71:100] = bad  # seen by rows 71.. of the second sequence, not by its first nor by the first sequence
+    got = qk.qk_attn_prompt(tq, tk, tv, i32(torch, cu))
+    n = np.r_[0:71]
+    _check(dtype, got[:71], *(a[n] for a in want), 70, dim)
+    assert torch.isnan(got[71:100].float()).all()
+
+
+def test_prompt_rows_outside_are_left_alone(torch_cuda):
+    torch = torch_cuda
+    q, k, v = (torch.randn(50, 2, 64, device="cuda") for _ in range(3))
+    out = torch.full_like(q, 9.0)
+    qk.qk_attn_prompt(q, k, v, i32(torch, [5, 20, 41]), out=out)
+    o = out.cpu()
+    assert (o[:5] == 9.0).all() and (o[41:] == 9.0).all() and not (o[5:41] == 9.0).any()
+    # key ranges beyond the keys are cut, not read
+    out2 = qk.qk_attn_prompt(q, k, v, i32(torch, [0, 50]), i32(torch, [10, 50]), causal=False)
+    out3 = qk.qk_attn_prompt(q, k, v, i32(torch, [0, 50]), i32(torch, [10, 900]), causal=False)
+    assert torch.equal(out2, out3)
+
+
+def test_prompt_in_a_graph(torch_cuda):
+    torch = torch_cuda
+    q, k, v = (torch.randn(300, n, 128, device="cuda", dtype=torch.bfloat16) for n in (8, 2, 2))
+    cu = i32(torch, [0, 100, 300])
+    qk.qk_attn_prompt(q, k, v, cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = qk.qk_attn_prompt(q, k, v, cu)
+    for mid in (100, 1, 299):
+        cu.copy_(torch.tensor([0, mid, 300], dtype=torch.int32))
+        q.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, qk.qk_attn_prompt(q, k, v, cu)), mid
+
+
+def test_chunked_prompt_through_the_cache(torch_cuda):
+    """Append a prompt in two chunks, read all of it back, attend the second chunk with the prompt
+    kernel: the same as attending it over the cache."""
+    torch = torch_cuda
+    rng = np.random.default_rng(31)
+    dim, hk, h, page = 128, 2, 8, 64
+    c = Cache(torch, rng, [230], hk, dim, page)
+    rope = torch.from_numpy(ref.rope_table(230, dim)).cuda()
+    q, k, v = (torch.randn(230, n, dim, device="cuda") for n in (h, hk, hk))
+    for a, b in ((0, 150), (150, 230)):
+        qr = qk.qk_kv_append(c.pages, page, c.dtable, i32(torch, [0, b - a]), i32(torch, [a]), k[a:b], v[a:b], q=q[a:b],
+                             rope=rope)
+    kk, vv = qk.qk_kv_read(c.pages, page, c.dtable, i32(torch, [0, 230]), i32(torch, [0]), 230, dim)
+    one = qk.qk_attn_prompt(qr, kk, vv, i32(torch, [0, 80]), i32(torch, [0, 230]))
+    two = qk.qk_attn_paged(c.pages, page, c.dtable, i32(torch, [0, 80]), i32(torch, [150]), qr)
+    c.raw = c.pages.cpu().numpy()
+    want = _paged_want(c, qr.double().cpu().numpy(), [80], [150], np.float64(np.float32(dim ** -0.5)), 0)
+    _check("f32", one, *want, 230, dim)
+    _check("f32", two, *want, 230, dim)
