@@ -28,6 +28,7 @@ namespace qk {
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -79,19 +80,44 @@ __device__ __forceinline__ int64_t page_of(const KvBatch& b, int seq, int64_t po
   return (page >= 0 && page < b.n_pages) ? page : -1;
 }
 
-// The 8 codes of a dword as f16 integers -8..7, in dim order: 0x6400 | n is 1024 + n and
-// 0x6400 | n << 4 is 1024 + 16 n, both exact; the subtraction and the multiply-add that
-// bring them to n - 8 are exact too.
-__device__ __forceinline__ half8 nibbles_to_f16(uint32_t w) {
+// Codes as f16 integers -8..7 from bits 0..3 (low) or 4..7 (high) of both halves of x: 0x6400 | n is
+// 1024 + n and 0x6400 | n << 4 is 1024 + 16 n, both exact; the subtraction and the multiply-add that
+// bring them to n - 8 are exact too.  The constants are kept in registers (a scalar and a
+// vector one) so that mask and OR are one v_and_or_b32, which takes no literals.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask) {
+  uint32_t magic = 0x64006400u;
+  asm("" : "+v"(magic));
+  asm("" : "+s"(mask));
+  return (x & mask) | magic;
+}
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t x) {
   const half2v off = {static_cast<_Float16>(-1032.0f), static_cast<_Float16>(-1032.0f)};
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, and_or(x, 0x000F000Fu)) + off);
+}
+__device__ __forceinline__ uint32_t high_nibbles(uint32_t x) {
   const half2v sixteenth = {static_cast<_Float16>(0.0625f), static_cast<_Float16>(0.0625f)};
-  const half2v off16 = {static_cast<_Float16>(-72.0f), static_cast<_Float16>(-72.0f)};
+  const half2v off = {static_cast<_Float16>(-72.0f), static_cast<_Float16>(-72.0f)};
+  return __builtin_bit_cast(uint32_t,
+                            __builtin_elementwise_fma(__builtin_bit_cast(half2v, and_or(x, 0x00F000F0u)), sixteenth, off));
+}
+// The 8 codes of a dword, in dim order.
+__device__ __forceinline__ half8 nibbles_to_f16(uint32_t w) {
   const uint32_t w8 = w >> 8;
-  const half2v h0 = __builtin_bit_cast(half2v, (w & 0x000F000Fu) | 0x64006400u) + off;
-  const half2v h1 = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (w & 0x00F000F0u) | 0x64006400u), sixteenth, off16);
-  const half2v h2 = __builtin_bit_cast(half2v, (w8 & 0x000F000Fu) | 0x64006400u) + off;
-  const half2v h3 = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (w8 & 0x00F000F0u) | 0x64006400u), sixteenth, off16);
-  return half8{h0.x, h0.y, h1.x, h1.y, h2.x, h2.y, h3.x, h3.y};
+  return __builtin_bit_cast(half8, uint4v{low_nibbles(w), high_nibbles(w), low_nibbles(w8), high_nibbles(w8)});
+}
+
+// Largest value and sum over the four lanes of equal lane % 16, returned in all of them.
+__device__ __forceinline__ float rows_max(float x) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float rows_sum(float x) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
 // 8 consecutive elements (16-byte aligned) as f32, and back with one rounding each.
