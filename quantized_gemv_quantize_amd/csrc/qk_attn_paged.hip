@@ -17,14 +17,15 @@
 // dword (lane % 4, block) of each position, one byte permute to a pair of positions.
 //
 // p = 2^(s - ref) with ref = m + E: m is a running maximum that moves only when a score passes it by
-// more than 8 (so no cross-lane maximum in most tiles).  E is 0 but for f16, where it is the power of two
-// that keeps w inside f16 for the value scales met so far, so that small value scales lose no bits.
+// more than 8 (so no cross-lane maximum in most tiles).  E is 0 for f32, else the power of two that
+// keeps w inside f16 for the value scales met so far, so that small value scales lose no bits.
 //
 // The score product is the same for every type: q is normalised to a power of two (bf16 then fits
-// f16) and f32 split into two f16 pieces, 22 bits.  The output product is of the type: weights are
-// rounded to f16 or bf16 (codes are exact in both), or stay f32 on mfma_16x16x4_f32.  A rounding to f16
-// would lose the weights of a bf16 or f32 row that are 2^-30 and less of the largest, which is all
-// that is left of a dim whose other values are 0.
+// f16) and f32 split into two f16 pieces, 22 bits.  In the output product f32 weights stay f32
+// (mfma_16x16x4_f32), f16 weights are rounded to f16, and so are those of bf16 unless the tile has one
+// so small that f16 would leave it less than bf16's 8 bits: weights 2^-32 and less of the largest are
+// all there is of a dim whose other values are 0.  Such a tile (and one with a mask or a scale of 0) is taken
+// in bf16, where turning the codes into bf16 costs 96 of some 400 vector instructions a tile.
 //
 // Work is split over the positions when the table allows more than kDirectSteps steps: all
 // items' steps laid end to end are cut into equal ranges, one a workgroup, however uneven
@@ -43,16 +44,26 @@ constexpr int kWaves = 4, kTile = 32, kStep = kWaves * kTile, kCols = 16;
 constexpr int kDirectSteps = 8;  // 1024 positions
 constexpr int kMinUnits = 3;     // least steps (the item's fixed cost counted as one) of a range
 
+// Workgroups that fit a CU by the registers of a lane (512 to a lane of the SIMD's wavefronts).
+constexpr int groups_per_cu(int dim) { return dim <= 64 ? 3 : (dim <= 128 ? 2 : 1); }
+
+struct JoinTask;
 struct PagedArgs {
   KvBatch b;
   const uint8_t* pages;
   const void* q;
   void* out;
-  float* part;  // workspace of the split, null: every workgroup takes one whole item
+  JoinTask* tasks;  // workspace of the split (n_wg tasks, then the parts), null: one whole item to a workgroup
   int64_t q_stride, window;
   int n_heads, group, n_wg;
   float scale;
 };
+
+// a / b for a >= 0, b > 0, mostly small.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 // Per-sequence work, the same for every item of the sequence.
 struct SeqWork {
@@ -79,7 +90,7 @@ __device__ __forceinline__ SeqWork seq_work(const PagedArgs& a, int64_t i) {
   if (hi <= lo) hi = lo = 0;
   s.lo = static_cast<int>(lo) & -kTile;
   s.hi = static_cast<int>(hi);
-  s.units = (s.hi - s.lo + kStep - 1) / kStep + 1;
+  s.units = static_cast<int>((static_cast<uint32_t>(s.hi - s.lo) + kStep - 1) / kStep) + 1;
   return s;
 }
 
@@ -140,42 +151,46 @@ __device__ __forceinline__ int find_seq(const PagedArgs& a, bool by_item, int64_
   return a.b.n_seq;
 }
 
-// How many workgroups share `total` units, and where the range of workgroup w begins.
-__device__ __forceinline__ int64_t ranges(int64_t total, int n_wg) {
-  const int64_t n = total / kMinUnits;
-  return n < 1 ? 1 : (n < n_wg ? n : n_wg);
-}
-__device__ __forceinline__ int64_t range_begin(int64_t total, int64_t n, int64_t w) { return w * total / n; }
+// `total` units cut into n ranges that differ by at most one unit.
+struct Ranges {
+  int64_t n, q, r;
+  __device__ Ranges(int64_t total, int n_wg) {
+    n = divide(total, kMinUnits);
+    n = n < 1 ? 1 : (n < n_wg ? n : n_wg);
+    q = divide(total, n), r = total - q * n;
+  }
+  __device__ int64_t begin(int64_t w) const { return w * q + (w < r ? w : r); }
+  __device__ int64_t holder(int64_t unit) const {
+    return unit < r * (q + 1) ? divide(unit, q + 1) : r + divide(unit - r * (q + 1), q);
+  }
+};
 
-// N consecutive dwords at a lane's offset from a wave-uniform one.  Buffer loads, because they take both
-// (and a page as their bound) without a 64-bit address in vector registers.
+// What the join does for the item that is cut at the end of a workgroup's range, where that range holds
+// the item's first units: its parts are the workgroup's part `slot` and part 0 of the next parts - 1.
+struct JoinTask {
+  int64_t row0, tile;
+  int32_t rows, kv, parts, slot;  // parts 0: nothing
+};
+constexpr int part_floats(int dim) { return dim / 16 * 256 + 128; }  // output registers, ref and sum of 64 lanes
+__device__ __forceinline__ float* part_at(const PagedArgs& a, int64_t w, int slot, int dim) {
+  return reinterpret_cast<float*>(a.tasks + a.n_wg) + (w * 2 + slot) * part_floats(dim);
+}
+
+// N consecutive dwords of LDS.
 template <int N>
-__device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t page, uint32_t lane, uint32_t at, uint32_t* o) {
+__device__ __forceinline__ void lds_dwords(const uint8_t* p, uint32_t* o) {
   if constexpr (N >= 4) {
-    const auto v = __builtin_amdgcn_raw_buffer_load_b128(page, lane, at, 0);
+    const uint4v v = *reinterpret_cast<const uint4v*>(p);
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[k] = v[k];
-    if constexpr (N > 4) load_dwords<N - 4>(page, lane + 16, at, o + 4);
-  } else if constexpr (N == 3) {
-    const auto v = __builtin_amdgcn_raw_buffer_load_b96(page, lane, at, 0);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) o[k] = v[k];
+    if constexpr (N > 4) lds_dwords<N - 4>(p + 16, o + 4);
   } else if constexpr (N == 2) {
-    const auto v = __builtin_amdgcn_raw_buffer_load_b64(page, lane, at, 0);
+    typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+    const uint2v v = *reinterpret_cast<const uint2v*>(p);
     o[0] = v[0], o[1] = v[1];
   } else {
-    o[0] = __builtin_amdgcn_raw_buffer_load_b32(page, lane, at, 0);
-  }
-}
-
-// Keeps what is computed from loaded registers behind this point, so that it is not moved up to
-// where the loads are still on the way.
-template <int M, int N>
-__device__ __forceinline__ void pin(uint32_t (&r)[M][N]) {
 #pragma unroll
-  for (int i = 0; i < M; ++i) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) asm volatile("" : "+v"(r[i][k]));
+    for (int k = 0; k < N; ++k) o[k] = reinterpret_cast<const uint32_t*>(p)[k];
   }
 }
 
@@ -223,35 +238,43 @@ __device__ __forceinline__ int out_dim(int b, int e, int i, int g) {
 
 // Column values of `a` (row and head), written where the item's column is one.
 template <typename T, int D>
-__device__ __forceinline__ void store_out(const PagedArgs& a, const SeqWork& s, int64_t tile, int kv, int b, int e,
+__device__ __forceinline__ void store_out(const PagedArgs& a, int64_t row0, int rows, int64_t tile, int kv, int b, int e,
                                           const float4v& v, float inv) {
   const int lane = threadIdx.x & 63, g = lane / 16;
   const int64_t at = tile * kCols + lane % 16;
-  if (at >= static_cast<int64_t>(s.rows) * a.group) return;
-  T* p = static_cast<T*>(a.out) + ((s.row0 + at / a.group) * a.n_heads + kv * a.group + at % a.group) * D;
+  if (at >= static_cast<int64_t>(rows) * a.group) return;
+  const int64_t row = divide(at, a.group);
+  T* p = static_cast<T*>(a.out) + ((row0 + row) * a.n_heads + kv * a.group + at - row * a.group) * D;
 #pragma unroll
   for (int i = 0; i < 4; ++i) p[out_dim(b, e, i, g)] = static_cast<T>(v[i] * inv);
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(PagedArgs a) {
+__global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(PagedArgs a) {
   constexpr int NB = D / 32, kRegs = NB * 2;  // float4 registers of the output
-  constexpr bool kF32T = std::is_same_v<T, float>, kF16T = std::is_same_v<T, _Float16>;
+  constexpr bool kF32T = std::is_same_v<T, float>, kBf16T = std::is_same_v<T, bf16>;
   constexpr int P = kF32T ? 2 : 1;  // f16 pieces of a query
-  __shared__ float4v so[kWaves][kRegs][64];
-  __shared__ float sref[kWaves][64], sl[kWaves][64];
+  // A wavefront's LDS: two tiles on their way from memory (each two halves of K codes, V codes, K
+  // scales, V scales), and in the same place its output registers for the joining of the four.
+  constexpr int kHalfBytes = 18 * D, kTileBytes = 2 * kHalfBytes, kWaveBytes = 2 * kTileBytes;
+  static_assert(kRegs * 1024 <= kWaveBytes);
+  __shared__ uint4v lds[kWaves * (kWaveBytes + 512) / 16];
+  // One array on purpose: with several the compiler sees LDS loads that may alias each other and waits for all
+  // loads before it reads any.
+  auto sref = reinterpret_cast<float(*)[64]>(lds + kWaves * kWaveBytes / 16), sl = sref + kWaves;
   const KvBatch& b = a.b;
   const int lane = threadIdx.x & 63, wave = wave_id(), col = lane % 16, g = lane / 16;
   const int64_t tokens = int64_t(1) << b.page_shift, half = kv_half_bytes(tokens, D);
-  const bool split = a.part != nullptr;
+  uint8_t* const ring = reinterpret_cast<uint8_t*>(lds) + wave * kWaveBytes;
+  const bool split = a.tasks != nullptr;
 
-  int64_t at, end, items0, units0, total = 0;
+  int64_t at, end, items0, units0;
   int seq;
+  const Ranges ranges(split ? total_units(a) : 1, a.n_wg);
   if (split) {
-    total = total_units(a);
-    const int64_t n = ranges(total, a.n_wg);
-    if (blockIdx.x >= n) return;
-    at = range_begin(total, n, blockIdx.x), end = range_begin(total, n, blockIdx.x + 1);
+    if (threadIdx.x == 0) a.tasks[blockIdx.x].parts = 0;
+    if (blockIdx.x >= ranges.n) return;
+    at = ranges.begin(blockIdx.x), end = ranges.begin(blockIdx.x + 1);
     seq = find_seq(a, false, at, &items0, &units0);
   } else {
     seq = find_seq(a, true, blockIdx.x, &items0, &units0);
@@ -270,18 +293,71 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
       if (++seq >= b.n_seq) return;
       continue;
     }
-    const int64_t item = first_lane((at - units0) / s.units);
-    const int u0 = __builtin_amdgcn_readfirstlane(static_cast<int>((at - units0) % s.units));
+    const int64_t item = first_lane(divide(at - units0, s.units));
+    const int u0 = __builtin_amdgcn_readfirstlane(static_cast<int>(at - units0 - item * s.units));
     const int u1 = static_cast<int>(end - at < s.units - u0 ? u0 + (end - at) : s.units);
-    const int kv = __builtin_amdgcn_readfirstlane(static_cast<int>(item / s.tiles));
-    const int64_t tile = first_lane(item % s.tiles);
+    const int kv = __builtin_amdgcn_readfirstlane(static_cast<int>(divide(item, s.tiles)));
+    const int64_t tile = first_lane(item - kv * s.tiles);
     const int k0 = u0 > 0 ? u0 - 1 : 0, k1 = u1 - 1;  // steps
+
+    // this wavefront's tiles: t0 + n * kStep
+    const int t0 = s.lo + k0 * kStep + wave * kTile;
+    const int64_t stop = static_cast<int64_t>(s.lo) + static_cast<int64_t>(k1) * kStep;
+    const int t_end = stop < s.hi ? static_cast<int>(stop) : s.hi;
+    const int n_tiles = t0 < t_end ? (t_end - t0 - 1) / kStep + 1 : 0;
+    int page_vec = -1;  // pages of the 16-position halves of tiles n & ~31 ..
+    const int32_t* table = b.table + static_cast<int64_t>(seq) * b.max_pages;
+    const int mask = static_cast<int>(tokens) - 1;
+    const int v_at = static_cast<int>(half), scales_at = static_cast<int>(tokens) * (D / 2);
+    bool bad[2], bad_next[2];
+    // Starts the loads of tile n into its place of the ring.
+    auto fetch = [&](int n) {
+      if ((n & 31) == 0) {
+        const int64_t p = t0 + static_cast<int64_t>(n + lane / 2) * kStep + (lane & 1) * 16;
+        page_vec = -1;
+        if (p < s.hi) {
+          const int32_t page = table[p >> b.page_shift];
+          if (page >= 0 && page < b.n_pages) page_vec = page;
+        }
+      }
+      // the LDS this writes was read by the tile before last: those reads have to be back
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int page = __builtin_amdgcn_readlane(page_vec, 2 * (n & 31) + h);
+        bad_next[h] = page < 0;  // page 0 is read in its place, and masked
+        uint8_t* p = const_cast<uint8_t*>(a.pages) + (static_cast<int64_t>(page < 0 ? 0 : page) * b.n_kv + kv) * 2 * half;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(p, 0, static_cast<int>(2 * half), 0x00027000);
+        const int slot = (t0 + n * kStep + 16 * h) & mask;
+        uint8_t* to = ring + (n & 1) * kTileBytes + h * kHalfBytes;
+        constexpr int kCodes = D / 2;  // 16-byte pieces of a half's codes, K or V
+        if constexpr (2 * kCodes <= 64) {
+          if (lane < 2 * kCodes)
+            load_to_lds(rsrc, to, lane < kCodes ? lane * 16 : (lane - kCodes) * 16 + v_at, slot * (D / 2));
+        } else {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+#pragma unroll
+            for (int c = 0; c < kCodes; c += 64) {
+              if (kCodes - c >= 64 || lane < kCodes - c)
+                load_to_lds(rsrc, to + (v * kCodes + c) * 16, (c + lane) * 16, slot * (D / 2) + v * v_at);
+            }
+          }
+        }
+        constexpr int kScales = 2 * NB;  // 16-byte pieces of a half's scales, K or V
+        if (lane < 2 * kScales)
+          load_to_lds(rsrc, to + 16 * D, lane < kScales ? lane * 16 : (lane - kScales) * 16 + v_at, scales_at + slot * (NB * 2));
+      }
+    };
+    // Load instructions of one fetch.
+    constexpr int kFetch = 2 * ((D <= 64 ? 1 : (D / 2 + 63) / 64 * 2) + 1);
+    if (n_tiles > 0) fetch(0);
 
     // the lane's column: its row's visible positions, its query normalised to 2^14 <= max < 2^15
     const int64_t cat = tile * kCols + col;
     const int64_t n_cols = static_cast<int64_t>(s.rows) * a.group;
     const bool real = cat < n_cols;
-    const int64_t row = real ? cat / a.group : 0;
+    const int64_t row = real ? divide(cat, a.group) : 0;
     const int64_t pos = s.pos0 + row;
     const int hi_q = static_cast<int>(pos < s.hi ? pos : s.hi - 1);
     const int lo_q = a.window > 0 && pos - a.window + 1 > 0 ? static_cast<int>(pos - a.window + 1) : 0;
@@ -289,7 +365,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
     float fac;
     {
       const T* p = static_cast<const T*>(a.q) + (s.row0 + row) * a.q_stride +
-                   (static_cast<int64_t>(kv) * a.group + (real ? cat % a.group : 0)) * D + 8 * g;
+                   (static_cast<int64_t>(kv) * a.group + (real ? cat - row * a.group : 0)) * D + 8 * g;
       float x[NB][8], top = 0.0f;
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk) {
@@ -313,8 +389,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
       }
     }
     // tiles in lo_max .. hi_min + 1 - kTile need no mask
-    const int64_t first = tile * kCols / a.group;
-    const int64_t last = ((tile + 1) * kCols < n_cols ? (tile + 1) * kCols - 1 : n_cols - 1) / a.group;
+    const int64_t first = divide(tile * kCols, a.group);
+    const int64_t last = divide((tile + 1) * kCols < n_cols ? (tile + 1) * kCols - 1 : n_cols - 1, a.group);
     const int64_t hi_min = s.pos0 + first < s.hi ? s.pos0 + first : s.hi - 1;
     const int64_t lo_max = a.window > 0 ? s.pos0 + last - a.window + 1 : 0;
 
@@ -324,59 +400,34 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
 #pragma unroll
     for (int i = 0; i < NB; ++i) st.o[i][0] = st.o[i][1] = float4v{0, 0, 0, 0};
 
-    // this wavefront's tiles: t0 + n * kStep
-    const int t0 = s.lo + k0 * kStep + wave * kTile;
-    const int t_end = s.lo + k1 * kStep < s.hi ? s.lo + k1 * kStep : s.hi;
-    const int n_tiles = t0 < t_end ? (t_end - t0 + kStep - 1) / kStep : 0;
-    int page_vec = -1;  // pages of the 16-position halves of tiles n & ~31 ..
-    const int32_t* table = b.table + static_cast<int64_t>(seq) * b.max_pages;
-    auto refill = [&](int n) {
-      const int64_t p = t0 + static_cast<int64_t>((n & ~31) + lane / 2) * kStep + (lane & 1) * 16;
-      page_vec = -1;
-      if (p < s.hi) {
-        const int32_t page = table[p >> b.page_shift];
-        if (page >= 0 && page < b.n_pages) page_vec = page;
-      }
-    };
-    constexpr int kHalf = 16;  // a tile is two halves of 16 positions, each inside one page
-    const int mask = static_cast<int>(tokens) - 1;
-    const uint32_t v_at = static_cast<uint32_t>(half), scales_at = static_cast<uint32_t>(tokens) * (D / 2);
-    // lane offsets from a half's first code or scale: its row of K codes, its 4 positions' scales, its dwords
-    // of the first of its 4 V rows, one dword of all the half's scales
-    const uint32_t k_lane = col * (D / 2) + g * NB * 4, d_lane = 4 * g * NB * 2, v_lane = 4 * g * (D / 2) + (col % 4) * NB * 4,
-                   top_lane = lane % (8 * NB) * 4;
-    uint32_t kc[2][NB], dk[2][2 * NB], vc[2][4][NB], dv[2][2 * NB], dt[2];
+    // lane offsets in a half: its row of K codes, its 4 positions' scales, its dwords of the first of its 4 V rows
+    const int k_lane = col * (D / 2) + g * NB * 4, d_lane = 4 * g * NB * 2, v_lane = 4 * g * (D / 2) + (col % 4) * NB * 4;
     const uint32_t sel = (col / 4) | 0x0C000C00u | (4 + col / 4) << 16;  // byte m of two dwords, each in a 16-bit half
     for (int n = 0; n < n_tiles; ++n) {
       const int t = t0 + n * kStep;
-      if ((n & 31) == 0) refill(n);
-      bool bad[2];
-      __amdgpu_buffer_rsrc_t rsrc[2];
+      bad[0] = bad_next[0], bad[1] = bad_next[1];
+      if (n + 1 < n_tiles) {
+        fetch(n + 1);
+        wait_loads<kFetch>();
+      } else {
+        wait_loads<0>();
+      }
+      const uint8_t* const in = ring + (n & 1) * kTileBytes;
+      // all of the tile's LDS reads at once: they are what the wavefront waits for
+      uint32_t kc[2][NB], dk[2][2 * NB], dv[2][2 * NB], vc[2][4][NB], dt[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int page = __builtin_amdgcn_readlane(page_vec, 2 * (n & 31) + h);
-        bad[h] = page < 0;  // page 0 is read in its place, and masked
-        const uint8_t* p = a.pages + (static_cast<int64_t>(page < 0 ? 0 : page) * b.n_kv + kv) * 2 * half;
-        rsrc[h] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, static_cast<int>(2 * half), 0x00027000);
+        lds_dwords<NB>(in + h * kHalfBytes + k_lane, kc[h]);
+        lds_dwords<2 * NB>(in + h * kHalfBytes + 16 * D + d_lane, dk[h]);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t slot = (t + kHalf * h) & mask;
-        load_dwords<NB>(rsrc[h], k_lane, slot * (D / 2), kc[h]);
-        load_dwords<2 * NB>(rsrc[h], d_lane, scales_at + slot * (NB * 2), dk[h]);
-      }
+        lds_dwords<2 * NB>(in + h * kHalfBytes + 16 * D + 32 * NB + d_lane, dv[h]);
+        if constexpr (!kF32T) lds_dwords<1>(in + h * kHalfBytes + 16 * D + 32 * NB + lane % (8 * NB) * 4, &dt[h]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t slot = (t + kHalf * h) & mask;
-        if constexpr (kF16T) load_dwords<1>(rsrc[h], top_lane, v_at + scales_at + slot * (NB * 2), &dt[h]);
-        load_dwords<2 * NB>(rsrc[h], d_lane, v_at + scales_at + slot * (NB * 2), dv[h]);
+        for (int i = 0; i < 4; ++i) lds_dwords<NB>(in + h * kHalfBytes + 8 * D + v_lane + i * (D / 2), vc[h][i]);
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t slot = (t + kHalf * h) & mask;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) load_dwords<NB>(rsrc[h], v_lane + i * (D / 2), v_at + slot * (D / 2), vc[h][i]);
-      }
+      __builtin_amdgcn_sched_barrier(0);
       float sc[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -393,11 +444,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[h][i] *= fac;
-        __builtin_amdgcn_sched_barrier(0);  // one half's products at a time in registers
       }
-      pin(dv);
       uint32_t dtop = 0;
-      if (t < lo_max || t + kTile > hi_min + 1 || bad[0] || bad[1]) {
+      const bool masked = t < lo_max || t + kTile > hi_min + 1 || bad[0] || bad[1];
+      if (masked) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           bool see[4];
@@ -407,26 +457,25 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
             see[i] = p <= hi_q && p >= lo_q && !bad[h];
             if (!see[i]) sc[h][i] = -INFINITY;
           }
-          // what a masked slot holds is not to be multiplied even by 0
+          if constexpr (!kF32T) {
 #pragma unroll
-          for (int k = 0; k < 2 * NB; ++k) {
-            dv[h][k] &= (see[2 * k / NB] ? 0xFFFFu : 0u) | (see[(2 * k + 1) / NB] ? 0xFFFF0000u : 0u);
-            if constexpr (kF16T) dtop = largest_half(dv[h][k], dtop);
+            for (int k = 0; k < 2 * NB; ++k)
+              dtop = largest_half(dv[h][k] & ((see[2 * k / NB] ? 0xFFFFu : 0u) | (see[(2 * k + 1) / NB] ? 0xFFFF0000u : 0u)), dtop);
           }
         }
-      } else if constexpr (kF16T) {
+      } else if constexpr (!kF32T) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) dtop = largest_half(dt[h], dtop);
+        for (int h = 0; h < 2; ++h) dtop = largest_half(dt[h], dtop);  // every value scale of the half once
       }
       float top = sc[0][0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[i / 4][i % 4]);
-      if (__any(top > st.lim || (kF16T && dtop > st.dlim))) {
+      if (__any(top > st.lim || (!kF32T && dtop > st.dlim))) {
         top = rows_max(top);
         st.m = fmaxf(st.m, top);
         st.lim = st.m + 8.0f;
         float ref = st.m;
-        if constexpr (kF16T) {
+        if constexpr (!kF32T) {
           const uint32_t dm = static_cast<uint32_t>(wave_max(static_cast<float>(dtop)));
           st.e16 = max(st.e16, dm >> 10);
           st.dlim = (st.e16 + 2) << 10;
@@ -448,36 +497,78 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
           st.l += p[h][i];
         }
       }
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk) {
-        float w[8];  // + 0: a multiply-add takes the f16 as it is (v_fma_mix_f32)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = fmaf(p[i / 4][i % 4], half_at(dv[i / 4], i % 4 * NB + blk), 0.0f);
-        uint32_t v0[4], v1[4];
+      // + 0: a multiply-add takes the f16 as it is (v_fma_mix_f32).  What a masked slot holds is not to be
+      // multiplied, not even by 0: it may be infinite or NaN.
+      auto weight = [&](int i, int blk) { return fmaf(p[i / 4][i % 4], half_at(dv[i / 4], i % 4 * NB + blk), 0.0f); };
+      auto masked_weight = [&](int i, int blk) { return p[i / 4][i % 4] == 0.0f ? 0.0f : weight(i, blk); };
+      auto codes = [&](int blk, uint32_t (&v0)[4], uint32_t (&v1)[4]) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t x = __builtin_amdgcn_perm(vc[k / 2][k % 2 * 2 + 1][blk], vc[k / 2][k % 2 * 2][blk], sel);
           v0[k] = low_nibbles(x);
           v1[k] = high_nibbles(x);
         }
-        if constexpr (kF32T) {
+      };
+      if constexpr (kF32T) {
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          uint32_t v0[4], v1[4];
+          codes(blk, v0, v1);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(half_at(v0, i), w[i], st.o[blk][0], 0, 0, 0);
-            st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(half_at(v1, i), w[i], st.o[blk][1], 0, 0, 0);
+            const float w = masked_weight(i, blk);
+            st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(half_at(v0, i), w, st.o[blk][0], 0, 0, 0);
+            st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(half_at(v1, i), w, st.o[blk][1], 0, 0, 0);
           }
-        } else if constexpr (kF16T) {
-          const half8 wf = pack8(w);
-          st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v0), wf, st.o[blk][0], 0, 0, 0);
-          st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v1), wf, st.o[blk][1], 0, 0, 0);
+        }
+      } else {
+        half8 wf[NB];
+        float least = FLT_MAX;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          float w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = weight(i, blk);
+          if constexpr (kBf16T) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) least = fminf(least, fabsf(w[i]));
+          }
+          wf[blk] = pack8(w);
+        }
+        // less than 8 bits left in f16
+        if (!(masked || (kBf16T && __any(least < 0x1p-17f)))) {
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) {
+            uint32_t v0[4], v1[4];
+            codes(blk, v0, v1);
+            st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v0), wf[blk], st.o[blk][0], 0, 0, 0);
+            st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v1), wf[blk], st.o[blk][1], 0, 0, 0);
+          }
         } else {
-          bf16x8 wf;
+          // weights once more: hidden, so that they are not kept in registers on the common path for this
 #pragma unroll
-          for (int i = 0; i < 8; ++i) wf[i] = static_cast<bf16>(w[i]);
+          for (int i = 0; i < 8; ++i) asm("" : "+v"(p[i / 4][i % 4]));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v0[k] = half_pair_to_bf16(v0[k]), v1[k] = half_pair_to_bf16(v1[k]);
-          st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<bf16x8>(v0), wf, st.o[blk][0], 0, 0, 0);
-          st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<bf16x8>(v1), wf, st.o[blk][1], 0, 0, 0);
+          for (int blk = 0; blk < NB; ++blk) {
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = masked_weight(i, blk);
+            uint32_t v0[4], v1[4];
+            codes(blk, v0, v1);
+            if constexpr (kBf16T) {
+              bf16x8 wb;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) wb[i] = static_cast<bf16>(w[i]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v0[k] = half_pair_to_bf16(v0[k]), v1[k] = half_pair_to_bf16(v1[k]);
+              st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<bf16x8>(v0), wb, st.o[blk][0], 0, 0, 0);
+              st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<bf16x8>(v1), wb, st.o[blk][1], 0, 0, 0);
+            } else {
+              const half8 wm = pack8(w);
+              st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v0), wm, st.o[blk][0], 0, 0, 0);
+              st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v1), wm, st.o[blk][1], 0, 0, 0);
+            }
+          }
         }
       }
     }
@@ -486,7 +577,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
     st.l = rows_sum(st.l);
     sref[wave][lane] = st.ref, sl[wave][lane] = st.l;
 #pragma unroll
-    for (int i = 0; i < kRegs; ++i) so[wave][i][lane] = st.o[i / 2][i % 2];
+    for (int i = 0; i < kRegs; ++i) reinterpret_cast<float4v*>(ring)[i * 64 + lane] = st.o[i / 2][i % 2];
     __syncthreads();
     float ref = sref[0][lane], l = 0.0f, f[kWaves];
 #pragma unroll
@@ -500,16 +591,20 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     float* part = nullptr;
     if (!whole) {
-      const int slot = units0 + item * s.units <= begin ? 0 : 1;
-      part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * (kRegs * 256 + 128);
+      const int slot = at == begin ? 0 : 1;
+      part = part_at(a, blockIdx.x, slot, D);
       if (wave == 0) part[lane] = ref, part[64 + lane] = l;
+      if (u0 == 0 && threadIdx.x == 0) {
+        const int64_t w = ranges.holder(units0 + (item + 1) * s.units - 1);
+        a.tasks[blockIdx.x] = JoinTask{s.row0, tile, s.rows, kv, static_cast<int32_t>(w - blockIdx.x + 1), slot};
+      }
     }
     for (int i = wave; i < kRegs; i += kWaves) {
       float4v v = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += so[w][i][lane] * f[w];
+      for (int w = 0; w < kWaves; ++w) v += reinterpret_cast<const float4v*>(lds)[w * (kWaveBytes / 16) + i * 64 + lane] * f[w];
       if (whole) {
-        store_out<T, D>(a, s, tile, kv, i / 2, i % 2, v, inv);
+        store_out<T, D>(a, s.row0, s.rows, tile, kv, i / 2, i % 2, v, inv);
       } else if (real) {
         reinterpret_cast<float4v*>(part + 128)[i * 64 + lane] = v;
       }
@@ -519,45 +614,61 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attn_paged_kernel(Paged
   }
 }
 
-// Workgroup (x, y): output register y of item x, joined from the ranges that hold parts of it.
+// Workgroup (x, y): output registers 2 y and 2 y + 1 of the item of task x, each wavefront over a
+// quarter of its parts.
 template <typename T, int D>
-__global__ __launch_bounds__(64) void attn_join_kernel(PagedArgs a) {
-  constexpr int kRegs = D / 16;
-  int64_t items0, units0;
-  const int lane = threadIdx.x;
-  const int64_t total = total_units(a);
-  const int64_t n = ranges(total, a.n_wg);
-  const int seq = find_seq(a, true, blockIdx.x, &items0, &units0);
-  if (seq >= a.b.n_seq) return;
-  const SeqWork s = seq_work(a, seq);
-  const int64_t item = blockIdx.x - items0;
-  const int64_t u0 = units0 + item * s.units, u1 = u0 + s.units;
-  int64_t w0 = u0 * n / total;
-  while (range_begin(total, n, w0 + 1) <= u0) ++w0;
-  if (range_begin(total, n, w0 + 1) >= u1) return;  // one range holds all of it
-  int64_t w1 = w0 + 1;
-  while (w1 < n && range_begin(total, n, w1) < u1) ++w1;
-  const int64_t tile = item % s.tiles;
-  auto part = [&](int64_t w) {
-    const int slot = u0 <= range_begin(total, n, w) ? 0 : 1;
-    return a.part + (w * 2 + slot) * (kRegs * 256 + 128);
-  };
+__global__ __launch_bounds__(256) void attn_join_kernel(PagedArgs a) {
+  __shared__ float4v so[kWaves][2][64];
+  __shared__ float sref[kWaves][64], sl[kWaves][64];
+  const JoinTask task = a.tasks[blockIdx.x];
+  if (task.parts == 0) return;
+  const int lane = threadIdx.x & 63, wave = wave_id(), y = blockIdx.y;
+  const bool real = task.tile * kCols + lane % 16 < static_cast<int64_t>(task.rows) * a.group;
+  auto part = [&](int i) { return part_at(a, blockIdx.x + i, i == 0 ? task.slot : 0, D); };
   float ref = -FLT_MAX, l = 0.0f;
-  for (int64_t w = w0; w < w1; ++w) ref = fmaxf(ref, part(w)[lane]);
-  float4v v = {0, 0, 0, 0};
-  if (tile * kCols + lane % 16 < static_cast<int64_t>(s.rows) * a.group) {
-    for (int64_t w = w0; w < w1; ++w) {
-      const float* p = part(w);
-      const float f = __builtin_amdgcn_exp2f(p[lane] - ref);
-      l += p[64 + lane] * f;
-      v += reinterpret_cast<const float4v*>(p + 128)[blockIdx.y * 64 + lane] * f;
+  float4v v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  // a batch of parts at a time: all its loads are on the way together
+  constexpr int kBatch = 8;
+  for (int i0 = wave; real && i0 < task.parts; i0 += kWaves * kBatch) {
+    float r[kBatch], s[kBatch], top = ref;
+    float4v x[kBatch][2];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kWaves;
+      const float* p = part(i < task.parts ? i : i0);
+      r[k] = i < task.parts ? p[lane] : -FLT_MAX;
+      s[k] = p[64 + lane];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) x[k][e] = reinterpret_cast<const float4v*>(p + 128)[(2 * y + e) * 64 + lane];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, r[k]);
+    const float keep = __builtin_amdgcn_exp2f(ref - top);
+    ref = top, l *= keep, v[0] *= keep, v[1] *= keep;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float f = i0 + k * kWaves < task.parts ? __builtin_amdgcn_exp2f(r[k] - ref) : 0.0f;
+      l += s[k] * f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) v[e] += x[k][e] * f;
     }
   }
-  store_out<T, D>(a, s, tile, static_cast<int>(item / s.tiles), blockIdx.y / 2, blockIdx.y % 2, v, l != 0.0f ? 1.0f / l : 0.0f);
+  sref[wave][lane] = ref, sl[wave][lane] = l;
+  so[wave][0][lane] = v[0], so[wave][1][lane] = v[1];
+  __syncthreads();
+  if (wave >= 2) return;
+  for (int w = 0; w < kWaves; ++w) ref = fmaxf(ref, sref[w][lane]);
+  l = 0.0f, v[0] = float4v{0, 0, 0, 0};
+  for (int w = 0; w < kWaves; ++w) {
+    const float f = __builtin_amdgcn_exp2f(sref[w][lane] - ref);
+    l += sl[w][lane] * f;
+    v[0] += so[w][wave][lane] * f;
+  }
+  store_out<T, D>(a, task.row0, task.rows, task.tile, task.kv, y, wave, v[0], l != 0.0f ? 1.0f / l : 0.0f);
 }
 
-// Workgroups that share the card in the split form: as many as run at once.
-int split_groups(int dim) { return 256 * (dim <= 128 ? 2 : 1); }
+// Workgroups of the split form: as many as run at once.
+int split_groups(int dim) { return 256 * groups_per_cu(dim); }
 
 // Most items a batch can have: every row with its group's heads, and a part-filled item to a sequence.
 int64_t max_items(const KvBatch& b, int n_heads) {
@@ -569,18 +680,16 @@ bool is_split(const KvBatch& b) { return (b.max_pages << b.page_shift) > kDirect
 
 template <typename T, int D>
 hipError_t run(const PagedArgs& a, hipStream_t s) {
-  unsigned gx = 0;
-  const int64_t items = max_items(a.b, a.n_heads);
-  if (a.part == nullptr) {
-    if (!launch_grid(items, 256, &gx)) return hipErrorInvalidConfiguration;
+  if (a.tasks == nullptr) {
+    unsigned gx = 0;
+    if (!launch_grid(max_items(a.b, a.n_heads), 256, &gx)) return hipErrorInvalidConfiguration;
     attn_paged_kernel<T, D><<<gx, 256, 0, s>>>(a);
     return hipGetLastError();
   }
-  if (!launch_grid(items * (D / 16), 64, &gx)) return hipErrorInvalidConfiguration;
   attn_paged_kernel<T, D><<<a.n_wg, 256, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attn_join_kernel<T, D><<<dim3(static_cast<unsigned>(items), D / 16), 64, 0, s>>>(a);
+  attn_join_kernel<T, D><<<dim3(a.n_wg, D / 32), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -597,12 +706,12 @@ hipError_t paged_t(const PagedArgs& a, int dim, hipStream_t s) {
 }  // namespace
 
 int64_t attn_paged_ws_bytes(const KvBatch& b, int dim, int) {
-  return is_split(b) ? static_cast<int64_t>(split_groups(dim)) * 2 * (dim / 16 * 256 + 128) * 4 : 0;
+  return is_split(b) ? split_groups(dim) * static_cast<int64_t>(sizeof(JoinTask) + 2 * part_floats(dim) * sizeof(float)) : 0;
 }
 
 hipError_t launch_attn_paged(const KvBatch& b, int dim, int dtype, const uint8_t* pages, const void* q, int64_t q_stride,
                              int n_heads, float scale, int64_t window, void* out, void* ws, hipStream_t s) {
-  const PagedArgs a{b, pages, q, out, is_split(b) ? static_cast<float*>(ws) : nullptr, q_stride, window, n_heads,
+  const PagedArgs a{b, pages, q, out, is_split(b) ? static_cast<JoinTask*>(ws) : nullptr, q_stride, window, n_heads,
                     n_heads / b.n_kv, split_groups(dim), scale};
   switch (dtype) {
     case kF32: return paged_t<float>(a, dim, s);

@@ -120,6 +120,17 @@ __device__ __forceinline__ float rows_sum(float x) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+// Starts a load of 16 bytes a lane from `rsrc` (offset `lane_at` a lane, `at` for all; zeros beyond its end)
+// to LDS, lane i's at `to` + 16 i.  Nothing but wait_loads waits for it: the compiler orders no LDS read behind it.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, void* to, int lane_at, int at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)to, 16, lane_at, at, 0, 0);
+}
+// Waits until at most N of the wavefront's loads are on the way; loads end in order.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // 8 consecutive elements (16-byte aligned) as f32, and back with one rounding each.
 __device__ __forceinline__ void load8(const float* p, float* v) {
   const float4v a = reinterpret_cast<const float4v*>(p)[0], b = reinterpret_cast<const float4v*>(p)[1];
