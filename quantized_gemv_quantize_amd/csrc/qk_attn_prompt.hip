@@ -1,79 +1,409 @@
 // qk_attn_prompt.hip - attention over whole packed prompts held as float q, k, v.
+//
+// The query rows of a sequence and the query heads that share a key / value head are one list of
+// columns (row x group + head of the group); a wavefront holds 32 of them, a workgroup
+// 32 x W, and walks the keys its rows see in tiles.  Keys and values of a tile come to LDS by
+// loads of their own (no registers), one tile ahead, and are shared by the W wavefronts.
+//
+// Both products have the columns as the matrix instruction's columns, so that a lane's column (lane %
+// 32) and its softmax state stay put:
+//   scores  S = K q       keys x dims   times  dims x columns
+//   output  O = V^T p     dims x keys   times  keys x columns
+// With h = lane / 32 the score registers 4 a + b of a lane are keys 8 a + 4 h + b of 32.  These are
+// taken as they are for the k-slots of the second product, so weights never change lanes; its other
+// operand (several keys of one dim) is read from LDS by the transposing load.
+//
+// p = 2^(c S - m): m is a running maximum that moves only when a score passes it by more than 8, so
+// most tiles need no maximum across lanes and no rescaling.  f32 runs on mfma_32x32x2_f32 throughout.
+//
+// A masked key's weight is 0, but 0 times an infinite or NaN value is NaN: a wavefront whose output is
+// not finite at the end computes its rows again key by key, over the visible keys only.
+#include <cfloat>
+#include <type_traits>
+
 #include "qk_internal.h"
 #include "qk_kv.h"
 
 namespace qk {
 namespace {
 
-// One wavefront per (row, head): 64 keys at a time, a lane's score each, then one dim per
-// lane over the 64 weights, with the running maximum and sum of the softmax.
+typedef float float16v __attribute__((ext_vector_type(16)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+
+constexpr int kCols = 32;
+
+struct PromptArgs {
+  PromptBatch b;
+  const void *q, *k, *v;
+  void* out;
+  int group;
+  float scale;
+};
+
+// LDS layout of a tile: rows of D elements in 16-byte pieces; piece p of row r lies at place p ^ swizzle(r), which
+// spreads what one load instruction reads over the banks.
 template <typename T, int D>
-__global__ __launch_bounds__(64) void attn_prompt_kernel(PromptBatch b, const T* q, const T* k, const T* v, float scale,
-                                                         T* out) {
-  __shared__ float sq[D], sp[64];
-  const int64_t row = blockIdx.x;
-  const int head = blockIdx.y, kv = head / (b.n_heads / b.n_kv), lane = threadIdx.x;
-  const int seq = row_seq(b.cu_q, b.n_seq, row);
-  if (seq >= b.n_seq || row < b.cu_q[seq]) return;
-  const int64_t q0 = b.cu_q[seq], q1 = b.cu_q[seq + 1];
-  int64_t k0 = b.cu_k[seq], k1 = b.cu_k[seq + 1];
-  k0 = k0 < 0 ? 0 : k0, k1 = k1 > b.n_k ? b.n_k : k1;
-  const int64_t len = k1 - k0, at = row - q0 + len - (q1 - q0);
-  const int64_t hi = b.causal ? (at + 1 < len ? at + 1 : len) : len;
-  const int64_t lo = (b.window > 0 && at - b.window + 1 > 0) ? at - b.window + 1 : 0;
-  for (int e = lane; e < D; e += 64) sq[e] = static_cast<float>(q[row * b.q_stride + head * D + e]) * scale;
-  float m = -INFINITY, l = 0.0f, o[(D + 63) / 64] = {};
-  for (int64_t t0 = lo; t0 < hi; t0 += 64) {
-    const int64_t t = t0 + lane;
-    float s = -INFINITY;
-    __syncthreads();
-    if (t < hi) {
-      s = 0.0f;
-      for (int e = 0; e < D; e += 8) {
-        float x[8];
-        load8(k + (k0 + t) * b.k_stride + kv * D + e, x);
+struct Tile {
+  static constexpr int kPer = 16 / sizeof(T);             // elements of a piece
+  static constexpr int kPieces = D / kPer;                // of a row
+  static constexpr int kRow = D * sizeof(T);              // bytes
+  static constexpr int kKeys = kRow <= 512 ? 64 : 32;     // two tiles of K and V in 128 KB
+  static constexpr int kBytes = kKeys * kRow;             // K or V
+  static constexpr int kLoads = kBytes / 1024;            // load instructions
+  // K: 32 rows at one piece.  Rows are 256 bytes apart (or 128, 512): 8 rows get 8 places; rows of 192 or 384
+  // bytes come in pairs, for which 4 places do.
+  __device__ static int k_swizzle(int r) { return D == 96 ? (r >> 1) & 3 : r & 7; }
+  // V: 4 rows at 64 bytes (16 bit), 2 rows 4 apart at 128 bytes (f32)
+  __device__ static int v_swizzle(int r) {
+    if (D == 96) return 0;
+    if (sizeof(T) == 4) return ((r >> 2) & 1) << 3;
+    return D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
+  }
+};
+
+// Sum of v over the wavefront, and the same as a scalar.
+__device__ __forceinline__ int wave_total(int v) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s += sq[e + j] * x[j];
-      }
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+// Column tiles of sequence i: its rows are kept inside 0 .. n_q.
+__device__ __forceinline__ int tiles_of(const PromptArgs& a, int i, int cols) {
+  int64_t c0 = a.b.cu_q[i], c1 = a.b.cu_q[i + 1];
+  if (c0 < 0) c0 = 0;
+  if (c1 > a.b.n_q) c1 = a.b.n_q;
+  return c1 > c0 ? static_cast<int>(((c1 - c0) * a.group + cols - 1) / cols) : 0;
+}
+
+// Workgroup t's sequence and tile.  The tiles of all sequences are ordered by their place in their
+// sequence, last first: a later tile sees more keys, and the longest work is not to start last.
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int cols, int t, int* seq, int* tile) {
+  const int lane = threadIdx.x & 63, n_seq = a.b.n_seq;
+  auto count = [&](int level) {  // tiles at place `level` and later
+    int n = 0;
+    for (int i = lane; i < n_seq; i += 64) {
+      const int m = tiles_of(a, i, cols) - level;
+      n += m > 0 ? m : 0;
     }
-    const float mt = fmaxf(m, wave_max(s));
-    const float p = t < hi ? expf(s - mt) : 0.0f;
-    const float keep = m == -INFINITY ? 0.0f : expf(m - mt);
-    l = l * keep + wave_sum(p);
-    m = mt;
-    sp[lane] = p;
-    __syncthreads();
+    return wave_total(n);
+  };
+  if (count(0) <= t) return false;
+  int most = 0;
+  for (int i = lane; i < n_seq; i += 64) most = max(most, tiles_of(a, i, cols));
 #pragma unroll
-    for (int i = 0; i < (D + 63) / 64; ++i) {
-      const int e = lane + 64 * i;
-      if (e >= D) break;
-      float a = o[i] * keep;
-      for (int u = 0; u < 64 && t0 + u < hi; ++u)
-        a += sp[u] * static_cast<float>(v[(k0 + t0 + u) * b.v_stride + kv * D + e]);
-      o[i] = a;
+  for (int d = 1; d < 64; d *= 2) most = max(most, __shfl_xor(most, d));
+  // count falls with the level: the last level at which it is above t
+  int lo = 0, hi = __builtin_amdgcn_readfirstlane(most), after = 0;  // count(lo) > t >= count(hi) = after
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2, n = count(mid);
+    if (n > t) {
+      lo = mid;
+    } else {
+      hi = mid, after = n;
     }
   }
-  for (int i = 0; i < (D + 63) / 64; ++i) {
-    const int e = lane + 64 * i;
-    if (e < D) out[(row * b.n_heads + head) * D + e] = static_cast<T>(l != 0.0f ? o[i] / l : 0.0f);
+  int k = t - after;  // the k-th sequence with a tile at place lo
+  for (int i = 0; i < n_seq; i += 64) {
+    const uint64_t has = __ballot(i + lane < n_seq && tiles_of(a, i + lane, cols) > lo);
+    const int n = __popcll(has);
+    if (k < n) {
+      const uint64_t below = has & ((uint64_t(1) << lane) - 1);
+      const uint64_t at = __ballot(((has >> lane) & 1) != 0 && __popcll(below) == k);
+      *seq = i + __builtin_ctzll(at), *tile = lo;
+      return true;
+    }
+    k -= n;
+  }
+  return false;
+}
+
+// One column, key by key.
+template <typename T, int D>
+__device__ __forceinline__ void column_by_keys(const T* q, const T* k, const T* v, int64_t k_stride, int64_t v_stride, int64_t lo,
+                                               int64_t hi, float c, T* out) {
+  const int lane = threadIdx.x & 63;
+  constexpr int N = (D + 63) / 64;
+  float m = -FLT_MAX, l = 0.0f, o[N] = {}, x[N] = {};
+  for (int i = 0; i < N; ++i) {
+    if (lane + 64 * i < D) x[i] = static_cast<float>(q[lane + 64 * i]);
+  }
+  for (int64_t t = lo; t < hi; ++t) {
+    float s = 0.0f;
+    for (int i = 0; i < N; ++i) {
+      if (lane + 64 * i < D) s += x[i] * static_cast<float>(k[t * k_stride + lane + 64 * i]);
+    }
+    s = wave_sum(s) * c;
+    const float top = fmaxf(m, s), keep = __builtin_amdgcn_exp2f(m - top), p = __builtin_amdgcn_exp2f(s - top);
+    m = top;
+    l = l * keep + p;
+    for (int i = 0; i < N; ++i) {
+      if (lane + 64 * i < D) o[i] = o[i] * keep + p * static_cast<float>(v[t * v_stride + lane + 64 * i]);
+    }
+  }
+  for (int i = 0; i < N; ++i) {
+    if (lane + 64 * i < D) out[lane + 64 * i] = static_cast<T>(l != 0.0f ? o[i] / l : 0.0f);
   }
 }
 
-template <typename T>
-hipError_t prompt_t(const PromptBatch& b, int dim, const void* q, const void* k, const void* v, float scale, void* out,
-                    hipStream_t s) {
-  unsigned gx = 0;
-  if (!launch_grid(b.n_q * b.n_heads, 64, &gx) || b.n_heads > 65535) return hipErrorInvalidConfiguration;
-  auto run = [&](auto kernel) {
-    kernel<<<dim3(static_cast<unsigned>(b.n_q), b.n_heads), 64, 0, s>>>(
-        b, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), scale, static_cast<T*>(out));
-    return hipGetLastError();
+template <typename T, int D, int W>
+__global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_prompt_kernel(PromptArgs a) {
+  using L = Tile<T, D>;
+  constexpr bool kF32T = std::is_same_v<T, float>;
+  constexpr int KT = L::kKeys, U = KT / 32, ND = D / 32;
+  constexpr int kSteps = kF32T ? D / 8 : D / 16;  // of the score product: two pieces of a key's row each
+  using Frag = std::conditional_t<kF32T, float4v, std::conditional_t<std::is_same_v<T, bf16>, bf16x8, half8>>;
+  static_assert(L::kLoads % W == 0);
+  __shared__ uint4v lds[4 * L::kBytes / 16];  // K, V, K, V
+  const PromptBatch& b = a.b;
+  const int lane = threadIdx.x & 63, wave = wave_id(), col = lane % 32, h = lane / 32;
+  const int kv = blockIdx.x % b.n_kv;
+  int seq, tile;
+  if (!find_tile(a, kCols * W, blockIdx.x / b.n_kv, &seq, &tile)) return;
+
+  // the sequence: query rows q0 .., keys k0 .. k0 + len - 1; row r stands at key r + at0
+  int64_t q0 = b.cu_q[seq], q1 = b.cu_q[seq + 1], k0 = b.cu_k[seq], k1 = b.cu_k[seq + 1];
+  k0 = k0 < 0 ? 0 : k0, k1 = k1 > b.n_k ? b.n_k : k1;
+  const int len = static_cast<int>(k1 > k0 ? k1 - k0 : 0);
+  int64_t at0 = (k1 - k0) - (q1 - q0);
+  if (q0 < 0) at0 -= q0, q0 = 0;
+  if (q1 > b.n_q) q1 = b.n_q;
+  const int rows = static_cast<int>(q1 - q0);
+  const int64_t n_cols = static_cast<int64_t>(rows) * a.group;
+  // keys lo .. hi - 1 that row r sees
+  auto hi_of = [&](int r) {
+    const int64_t hi = b.causal ? r + at0 + 1 : len;
+    return static_cast<int>(hi < 0 ? 0 : (hi < len ? hi : len));
   };
+  auto lo_of = [&](int r) {
+    const int64_t lo = b.window > 0 ? r + at0 - b.window + 1 : 0;
+    return static_cast<int>(lo < 0 ? 0 : (lo < len ? lo : len));
+  };
+  auto row_of = [&](int64_t c) { return static_cast<int>((c < n_cols ? c : n_cols - 1) / a.group); };
+  const int64_t wg_col = static_cast<int64_t>(tile) * kCols * W, my_col = wg_col + wave * kCols;
+  const int wg_hi = hi_of(row_of(wg_col + kCols * W - 1)), wg_lo = lo_of(row_of(wg_col)) & -KT;
+  const int first = row_of(my_col), last = row_of(my_col + kCols - 1);
+  const bool idle = my_col >= n_cols;
+  const int hi_max = idle ? 0 : hi_of(last), hi_min = hi_of(first), lo_min = lo_of(first), lo_max = lo_of(last);
+  const int64_t c_at = my_col + col;
+  const int row = row_of(c_at), hi_q = hi_of(row), lo_q = lo_of(row);
+  const int head = kv * a.group + static_cast<int>((c_at < n_cols ? c_at : n_cols - 1) - static_cast<int64_t>(row) * a.group);
+  // a negative scale turns q around, so that the largest product is the largest score
+  const float c = fabsf(a.scale) * 1.4426950408889634f;
+
+  // loads of a tile: instruction j of this wavefront fills 1 KB from row (j W + wave) 1024 / kRow on
+  constexpr int kMine = L::kLoads / W;
+  uint32_t k_at[kMine], v_at[kMine];
+  const uint32_t ks = static_cast<uint32_t>(b.k_stride * sizeof(T)), vs = static_cast<uint32_t>(b.v_stride * sizeof(T));
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int piece = (j * W + wave) * 64 + lane, r = piece / L::kPieces, p = piece % L::kPieces;
+    k_at[j] = r * ks + (p ^ L::k_swizzle(r)) * 16;
+    v_at[j] = r * vs + (p ^ L::v_swizzle(r)) * 16;
+  }
+  const T* const k_base = static_cast<const T*>(a.k) + k0 * b.k_stride + kv * D;
+  const T* const v_base = static_cast<const T*>(a.v) + k0 * b.v_stride + kv * D;
+  uint8_t* const lds8 = reinterpret_cast<uint8_t*>(lds);
+  auto fetch = [&](int t, int buf) {
+    const int n = len - t < KT ? len - t : KT;  // rows that are keys; the rest is zeros
+    auto kr = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(k_base + t * b.k_stride), 0, (n - 1) * ks + L::kRow, 0x00027000);
+    auto vr = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(v_base + t * b.v_stride), 0, (n - 1) * vs + L::kRow, 0x00027000);
+    uint8_t* to = lds8 + buf * 2 * L::kBytes;
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) load_to_lds(kr, to + (j * W + wave) * 1024, k_at[j], 0);
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) load_to_lds(vr, to + L::kBytes + (j * W + wave) * 1024, v_at[j], 0);
+  };
+  const int tiles = wg_hi > wg_lo ? (wg_hi - wg_lo + KT - 1) / KT : 0;
+  if (tiles > 0) fetch(wg_lo, 0);
+
+  Frag qf[kSteps];
+  {
+    const T* p = static_cast<const T*>(a.q) + (q0 + row) * b.q_stride + static_cast<int64_t>(head) * D + h * L::kPer;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      qf[s] = *reinterpret_cast<const Frag*>(p + s * 2 * L::kPer);
+      if (a.scale < 0.0f) qf[s] = -qf[s];
+    }
+  }
+  // places in LDS: piece 2 s + h of K row col; the V pieces of dims 32 d ..
+  int k_lds[kSteps], v_lds[ND];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) k_lds[s] = col * L::kRow + ((2 * s + h) ^ L::k_swizzle(col)) * 16;
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+    if constexpr (kF32T) {
+      v_lds[d] = 4 * h * L::kRow + ((8 * d + col / 4) ^ L::v_swizzle(4 * h)) * 16 + col % 4 * 4;
+    } else {
+      const int i = lane % 16, r = 4 * h + i / 4, p = 4 * d + 2 * (lane / 16 % 2) + i % 4 / 2;
+      v_lds[d] = r * L::kRow + (p ^ L::v_swizzle(r)) * 16 + i % 2 * 8;
+    }
+  }
+
+  float m = -FLT_MAX, lim = -FLT_MAX, l = 0.0f;
+  float16v o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  }
+  for (int n = 0; n < tiles; ++n) {
+    const int t = wg_lo + n * KT;
+    wait_loads<0>();
+    __syncthreads();
+    if (n + 1 < tiles) fetch(t + KT, (n + 1) & 1);
+    if (t >= hi_max || t + KT <= lo_min) continue;
+    const uint8_t* const kt = lds8 + (n & 1) * 2 * L::kBytes;
+    const uint8_t* const vt = kt + L::kBytes;
+    float16v s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        const Frag kf = *reinterpret_cast<const Frag*>(kt + u * 32 * L::kRow + k_lds[j]);
+        if constexpr (kF32T) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[u] = __builtin_amdgcn_mfma_f32_32x32x2f32(kf[e], qf[j][e], s[u], 0, 0, 0);
+        } else if constexpr (std::is_same_v<T, bf16>) {
+          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], s[u], 0, 0, 0);
+        } else {
+          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[j], s[u], 0, 0, 0);
+        }
+      }
+    }
+    if (t + KT > hi_min || t < lo_max) {
+      const int lo = lo_q - t - 4 * h, hi = hi_q - t - 4 * h;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int k = 32 * u + 8 * (i / 4) + i % 4;
+          if (k < lo || k >= hi) s[u][i] = -INFINITY;
+        }
+      }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 16 * U; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+    top *= c;
+    if (__any(top > lim)) {
+      const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+      const float next = fmaxf(m, fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])));
+      const float keep = __builtin_amdgcn_exp2f(m - next);
+      m = next, lim = m + 8.0f;
+      l *= keep;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] *= keep;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], c, -m));
+        l += s[u][i];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (kF32T) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const float vf = *reinterpret_cast<const float*>(vt + (32 * u + 8 * (i / 4) + i % 4) * L::kRow + v_lds[d]);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, s[u][i], o[d], 0, 0, 0);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          Frag pf;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pf[i] = static_cast<T>(s[u][8 * g + i]);
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            typedef __attribute__((address_space(3))) short4v lds_short4;
+            const uint8_t* p = vt + (32 * u + 16 * g) * L::kRow + v_lds[d];
+            const short4v v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)p);
+            const short4v v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(p + 8 * L::kRow));
+            const Frag vf = __builtin_bit_cast(Frag, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+            if constexpr (std::is_same_v<T, bf16>) {
+              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
+            } else {
+              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf, o[d], 0, 0, 0);
+            }
+          }
+        }
+      }
+    }
+  }
+  if (idle) return;
+
+  const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+  l = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  bool finite = true;
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      o[d][i] *= inv;
+      finite = finite && fabsf(o[d][i]) <= FLT_MAX;
+    }
+  }
+  if (__any(!finite)) {
+    for (int i = 0; i < kCols && my_col + i < n_cols; ++i) {
+      const int r = row_of(my_col + i);
+      const int64_t hd = static_cast<int64_t>(kv) * a.group + (my_col + i - static_cast<int64_t>(r) * a.group);
+      column_by_keys<T, D>(static_cast<const T*>(a.q) + (q0 + r) * b.q_stride + hd * D, k_base, v_base, b.k_stride, b.v_stride,
+                           lo_of(r), hi_of(r), a.scale * 1.4426950408889634f,
+                           static_cast<T*>(a.out) + ((q0 + r) * b.n_heads + hd) * D);
+    }
+    return;
+  }
+  if (c_at >= n_cols) return;
+  T* out = static_cast<T*>(a.out) + ((q0 + row) * b.n_heads + head) * D + 4 * h;
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      typedef T t4 __attribute__((ext_vector_type(4)));
+      t4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = static_cast<T>(o[d][4 * i + e]);
+      *reinterpret_cast<t4*>(out + 32 * d + 8 * i) = x;
+    }
+  }
+}
+
+template <typename T, int D, int W>
+hipError_t run(const PromptArgs& a, hipStream_t s) {
+  // every column, and a part-filled tile to a sequence
+  const int64_t seqs = a.b.n_seq < a.b.n_q ? a.b.n_seq : a.b.n_q;
+  const int64_t tiles = a.b.n_q * a.group / (kCols * W) + seqs;
+  unsigned gx = 0;
+  if (tiles > INT32_MAX / 64 || !launch_grid(tiles * a.b.n_kv, 64 * W, &gx)) return hipErrorInvalidConfiguration;
+  attn_prompt_kernel<T, D, W><<<gx, 64 * W, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t prompt_w(const PromptArgs& a, hipStream_t s) {
+  // wavefronts of a workgroup: few workgroups are better small
+  const int64_t cols = a.b.n_q * a.b.n_heads;
+  constexpr int kWide = D <= 128 ? (D == 96 ? 4 : 8) : 4;
+  return cols >= 256 * kCols * kWide ? run<T, D, kWide>(a, s) : run<T, D, 2>(a, s);
+}
+
+template <typename T>
+hipError_t prompt_t(const PromptArgs& a, int dim, hipStream_t s) {
   switch (dim) {
-    case 64: return run(attn_prompt_kernel<T, 64>);
-    case 96: return run(attn_prompt_kernel<T, 96>);
-    case 128: return run(attn_prompt_kernel<T, 128>);
-    default: return run(attn_prompt_kernel<T, 256>);
+    case 64: return prompt_w<T, 64>(a, s);
+    case 96: return prompt_w<T, 96>(a, s);
+    case 128: return prompt_w<T, 128>(a, s);
+    default: return prompt_w<T, 256>(a, s);
   }
 }
 
@@ -81,10 +411,11 @@ hipError_t prompt_t(const PromptBatch& b, int dim, const void* q, const void* k,
 
 hipError_t launch_attn_prompt(const PromptBatch& b, int dim, int dtype, const void* q, const void* k, const void* v,
                               float scale, void* out, hipStream_t s) {
+  const PromptArgs a{b, q, k, v, out, b.n_heads / b.n_kv, scale};
   switch (dtype) {
-    case kF32: return prompt_t<float>(b, dim, q, k, v, scale, out, s);
-    case kF16: return prompt_t<_Float16>(b, dim, q, k, v, scale, out, s);
-    default: return prompt_t<bf16>(b, dim, q, k, v, scale, out, s);
+    case kF32: return prompt_t<float>(a, dim, s);
+    case kF16: return prompt_t<_Float16>(a, dim, s);
+    default: return prompt_t<bf16>(a, dim, s);
   }
 }
 
