@@ -6,7 +6,6 @@ the C names and only marshal arguments: torch tensors supply device pointers
 and the current stream; every step of the computation runs in the HIP kernels.
 There is no fallback: if libqk.so is missing or cannot be loaded, calls raise.
 """
-import contextlib
 import ctypes
 import os
 
@@ -278,38 +277,69 @@ def qk_gemv_pair_timed(w_type, W1, W2, n_out, n_in, xq, ncols, epilogue, out, ev
     return out
 
 
+# The attention calls are made once per layer and token, so what they cost here counts: about
+# 5 us of checks and marshalling beside the 4 us of a kernel launch.
+_float_types = {}
+
+
 def _float_type(dtype):
-    import torch
-    t = {torch.float32: QK_TYPE_F32, torch.float16: QK_TYPE_F16, torch.bfloat16: QK_TYPE_BF16}.get(dtype)
+    t = _float_types.get(dtype)
     if t is None:
-        raise TypeError(f"dtype {dtype}: the attention calls take float32, float16 and bfloat16")
+        import torch
+        _float_types.update({torch.float32: QK_TYPE_F32, torch.float16: QK_TYPE_F16, torch.bfloat16: QK_TYPE_BF16})
+        t = _float_types.get(dtype)
+        if t is None:
+            raise TypeError(f"dtype {dtype}: the attention calls take float32, float16 and bfloat16")
     return t
+
+
+def _current_stream(stream):
+    """The stream's handle; without one, that of the current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    try:  # torch.cuda.current_stream() makes an object of it, which takes 10 times as long
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _heads(t, what, dtype):
     """(rows, heads, head dim, row stride) of a [rows, heads, D] tensor whose rows may be strided."""
     if t.dtype != dtype:
         raise TypeError(f"{what} is {t.dtype}, not {dtype}")
-    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
-        raise ValueError(f"{what}: [rows, heads, head dim] with contiguous rows, not shape {tuple(t.shape)} "
-                         f"strides {t.stride()}")
-    n, h, d = t.shape
-    return n, h, d, t.stride(0) if n > 1 else h * d
+    if t.dim() == 3:
+        n, h, d = t.shape
+        if t.is_contiguous():
+            return n, h, d, h * d
+        s0, s1, s2 = t.stride()
+        if not t.numel() or (s2 == 1 and (s1 == d or h == 1)):
+            return n, h, d, s0 if n > 1 else h * d
+    raise ValueError(f"{what}: [rows, heads, head dim] with contiguous rows, not shape {tuple(t.shape)} "
+                     f"strides {t.stride()}")
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _index(t, what, shape):
     import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: contiguous int32 {list(shape)}, not {t.dtype} {list(t.shape)}")
     return t.data_ptr()
 
 
-def _result(t, what, shape, like, dtype):
-    """The caller's output tensor, checked, or a new one."""
-    import torch
+def _result(t, what, shape, like, dtype, stream):
+    """The caller's output tensor, checked, or a new one.  A new one is allocated under the stream that
+    writes it: memory of another stream's pool may still be in use there."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        if stream is None:
+            return like.new_empty(shape, dtype=dtype)
+        import torch
+        with torch.cuda.stream(stream):
+            return like.new_empty(shape, dtype=dtype)
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: contiguous {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
     return t
 
@@ -323,7 +353,8 @@ def _kv_batch(pages, page_tokens, page_table, cu, start, n_rows, head_dim):
     if page_table.dim() != 2:
         raise ValueError(f"page_table: int32 [sequences, pages], not {list(page_table.shape)}")
     n_seq, max_pages = page_table.shape
-    return _KVBatch(QK_TYPE_Q4_0, page_tokens, pages.shape[0], pages.shape[1], head_dim,
+    n_pages, n_kv, _ = pages.shape
+    return _KVBatch(QK_TYPE_Q4_0, page_tokens, n_pages, n_kv, head_dim,
                     _index(page_table, "page_table", (n_seq, max_pages)), max_pages, _index(cu, "cu", (n_seq + 1,)),
                     _index(start, "start", (n_seq,)), n_seq, n_rows)
 
@@ -339,7 +370,6 @@ def qk_kv_append(pages, page_tokens, page_table, cu, start, k, v, q=None, rope=N
     page_table int32 [sequences, pages], cu int32 [sequences + 1] and start int32 [sequences] say
     where the rows go.  rope: f32 [positions, n_rot / 2, 2] (cos, sin), None for no rotation.
     Returns the rotated queries, None without q."""
-    import torch
     n, hk, d, ks = _heads(k, "k", k.dtype)
     nv, hv, dv, vs = _heads(v, "v", k.dtype)
     if (nv, hv, dv) != (n, hk, d) or hk != pages.shape[1]:
@@ -350,47 +380,46 @@ def qk_kv_append(pages, page_tokens, page_table, cu, start, k, v, q=None, rope=N
         nq, h, dq, qs = _heads(q, "q", k.dtype)
         if (nq, dq) != (n, d):
             raise ValueError(f"q {list(q.shape)}, k {list(k.shape)}")
-        q_out = _result(q_out, "q_out", (n, h, d), q, k.dtype)
+        q_out = _result(q_out, "q_out", (n, h, d), q, k.dtype, stream)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or
-                             not rope.is_contiguous()):
-        raise ValueError(f"rope: contiguous float32 [positions, n_rot / 2, 2], not {rope.dtype} {list(rope.shape)}")
-    rows, rot = (rope.shape[0], 2 * rope.shape[1]) if rope is not None else (0, 0)
-    _check(lib().qk_kv_append(b, pages.data_ptr(), t, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, h, _ptr(rope), rows,
-                              rot, rope_style, _ptr(q_out), _stream(stream)), "qk_kv_append")
+    rows, rot = 0, 0
+    if rope is not None:
+        if _float_type(rope.dtype) != QK_TYPE_F32 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous():
+            raise ValueError(f"rope: contiguous float32 [positions, n_rot / 2, 2], not {rope.dtype} {list(rope.shape)}")
+        rows, rot = rope.shape[0], 2 * rope.shape[1]
+    _check(lib().qk_kv_append(b, pages.data_ptr(), t, k.data_ptr(), ks, v.data_ptr(), vs, _address(q), qs, h, _address(rope),
+                              rows, rot, rope_style, _address(q_out), _current_stream(stream)), "qk_kv_append")
     return q_out
 
 
 def qk_kv_read(pages, page_tokens, page_table, cu, start, n_rows, head_dim, dtype=None, k_out=None, v_out=None,
                stream=None):
     """(k, v), each [n_rows, kv heads, head_dim] of `dtype` (float32 where none is given), of cached rows."""
-    import torch
-    dtype = dtype or (k_out.dtype if k_out is not None else torch.float32)
+    if dtype is None:
+        import torch
+        dtype = k_out.dtype if k_out is not None else torch.float32
     b = _kv_batch(pages, page_tokens, page_table, cu, start, n_rows, head_dim)
     shape = (n_rows, pages.shape[1], head_dim)
-    k_out = _result(k_out, "k_out", shape, pages, dtype)
-    v_out = _result(v_out, "v_out", shape, pages, dtype)
+    k_out = _result(k_out, "k_out", shape, pages, dtype, stream)
+    v_out = _result(v_out, "v_out", shape, pages, dtype, stream)
     _check(lib().qk_kv_read(b, pages.data_ptr(), _float_type(dtype), k_out.data_ptr(), v_out.data_ptr(),
-                            _stream(stream)), "qk_kv_read")
+                            _current_stream(stream)), "qk_kv_read")
     return k_out, v_out
 
 
 def qk_attn_paged(pages, page_tokens, page_table, cu, start, q, scale=None, window=0, out=None, ws=None, stream=None):
     """Attention of the rows of q [rows, heads, D] over the cache up to each row's own position; scale
     is 1 / sqrt(D) where none is given.  ws: a uint8 workspace to reuse (allocated when None)."""
-    import torch
     n, h, d, qs = _heads(q, "q", q.dtype)
     b = _kv_batch(pages, page_tokens, page_table, cu, start, n, d)
-    out = _result(out, "out", (n, h, d), q, q.dtype)
+    out = _result(out, "out", (n, h, d), q, q.dtype, stream)
     need = int(lib().qk_attn_paged_ws_bytes(b, h))
     if ws is None and need:
-        # the allocator ties the workspace to the stream that is current here
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
+        ws = _result(None, "ws", (need,), pages, pages.dtype, stream)
     _check(lib().qk_attn_paged(b, pages.data_ptr(), _float_type(q.dtype), q.data_ptr(), qs, h,
-                               d ** -0.5 if scale is None else scale, window, out.data_ptr(), _ptr(ws),
-                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "qk_attn_paged")
+                               d ** -0.5 if scale is None else scale, window, out.data_ptr(), _address(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), _current_stream(stream)), "qk_attn_paged")
     return out
 
 
@@ -406,10 +435,10 @@ def qk_attn_prompt(q, k, v, cu_q, cu_k=None, scale=None, causal=True, window=0, 
     n_seq = cu_q.numel() - 1
     pq = _index(cu_q, "cu_q", (n_seq + 1,))
     pk = pq if cu_k is None else _index(cu_k, "cu_k", (n_seq + 1,))
-    out = _result(out, "out", (n, h, d), q, q.dtype)
+    out = _result(out, "out", (n, h, d), q, q.dtype, stream)
     _check(lib().qk_attn_prompt(_float_type(q.dtype), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, pq, pk, n_seq, n,
                                 nk, h, hk, d, d ** -0.5 if scale is None else scale, int(causal), window,
-                                out.data_ptr(), _stream(stream)), "qk_attn_prompt")
+                                out.data_ptr(), _current_stream(stream)), "qk_attn_prompt")
     return out
 
 

@@ -442,6 +442,32 @@ def test_calls_on_another_stream_and_in_a_graph(torch_cuda):
         assert torch.equal(pages, eager), i
 
 
+def test_calls_take_a_stream(torch_cuda):
+    """Every call on a stream handed to it, its outputs and workspace its own: as on the current stream."""
+    torch = torch_cuda
+    rng = np.random.default_rng(14)
+    dim, hk, h, page = 64, 2, 4, 16
+    c = Cache(torch, rng, [3000, 90], hk, dim, page)
+    k, v, q = (torch.randn(2, n, dim, device="cuda") for n in (hk, hk, h))
+    rope = torch.from_numpy(ref.rope_table(3000, dim)).cuda()
+    cu, start = i32(torch, [0, 1, 2]), i32(torch, [2999, 50])
+
+    def step(pages, stream=None):
+        at = (pages, page, c.dtable, cu, start)
+        qr = qk.qk_kv_append(*at, k, v, q=q, rope=rope, stream=stream)
+        kk, vv = qk.qk_kv_read(*at, 2, dim, stream=stream)
+        return (qr, kk, vv, qk.qk_attn_paged(*at, qr, stream=stream), qk.qk_attn_prompt(qr, kk, vv, cu, stream=stream))
+
+    want = step(c.pages.clone())
+    pages = c.pages.clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = step(pages, side)
+    side.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------------------
 # attention over prompts
 
