@@ -42,7 +42,8 @@ namespace {
 
 constexpr int kWaves = 4, kTile = 32, kStep = kWaves * kTile, kCols = 16;
 constexpr int kDirectSteps = 8;  // 1024 positions
-constexpr int kMinUnits = 3;     // least steps (the item's fixed cost counted as one) of a range
+constexpr int kFixedUnits = 2;   // an item's start and end cost about as much as 2 of its steps
+constexpr int kMinUnits = 3;     // least units of a range
 
 // Workgroups that fit a CU by the registers of a lane (512 to a lane of the SIMD's wavefronts).
 constexpr int groups_per_cu(int dim) { return dim <= 64 ? 3 : (dim <= 128 ? 2 : 1); }
@@ -70,7 +71,7 @@ struct SeqWork {
   int64_t row0, pos0;  // first packed row, its position
   int64_t tiles;       // items per key / value head
   int rows, lo, hi;    // positions lo (a multiple of kTile) .. hi - 1 are visited
-  int units;           // steps + 1
+  int units;           // steps + kFixedUnits
 };
 
 __device__ __forceinline__ SeqWork seq_work(const PagedArgs& a, int64_t i) {
@@ -90,7 +91,7 @@ __device__ __forceinline__ SeqWork seq_work(const PagedArgs& a, int64_t i) {
   if (hi <= lo) hi = lo = 0;
   s.lo = static_cast<int>(lo) & -kTile;
   s.hi = static_cast<int>(hi);
-  s.units = static_cast<int>((static_cast<uint32_t>(s.hi - s.lo) + kStep - 1) / kStep) + 1;
+  s.units = static_cast<int>((static_cast<uint32_t>(s.hi - s.lo) + kStep - 1) / kStep) + kFixedUnits;
   return s;
 }
 
@@ -110,46 +111,61 @@ __device__ __forceinline__ int64_t first_lane(int64_t v) {
   return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
-// Units of all items.
-__device__ __forceinline__ int64_t total_units(const PagedArgs& a) {
-  const int lane = threadIdx.x & 63;
-  int64_t sum = 0;
-  for (int i = 0; i < a.b.n_seq; i += 64) {
-    int64_t w = 0;
-    if (i + lane < a.b.n_seq) {
-      const SeqWork s = seq_work(a, i + lane);
-      w = s.tiles * s.units;
-    }
-    sum += __shfl(wave_scan(w), 63);
-  }
-  return first_lane(sum) * a.b.n_kv;
+__device__ __forceinline__ int read_lane(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ int64_t read_lane(int64_t v, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), l);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), l);
+  return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
-// The sequence whose share of the items (by_item) or of the units holds `at`; `items0` and `units0`
-// are what comes before it.  n_seq when there is none.
-__device__ __forceinline__ int find_seq(const PagedArgs& a, bool by_item, int64_t at, int64_t* items0, int64_t* units0) {
-  const int lane = threadIdx.x & 63;
-  int64_t items = 0, units = 0;
-  for (int i = 0; i < a.b.n_seq; i += 64) {
-    int64_t n = 0, w = 0;
-    if (i + lane < a.b.n_seq) {
-      const SeqWork s = seq_work(a, i + lane);
-      n = s.tiles * a.b.n_kv;
-      w = n * s.units;
-    }
-    const int64_t ni = wave_scan(n), wi = wave_scan(w);
-    const uint64_t hit = __ballot((by_item ? items + ni : units + wi) > at);
-    if (hit != 0) {
-      const int l = __builtin_ctzll(hit);
-      *items0 = first_lane(items + __shfl(ni - n, l));
-      *units0 = first_lane(units + __shfl(wi - w, l));
-      return __builtin_amdgcn_readfirstlane(i + l);
-    }
-    items += __shfl(ni, 63);
-    units += __shfl(wi, 63);
+// The sequences' shares of items and units, 64 sequences at a time; the first 64 stay in registers.
+struct Shares {
+  SeqWork first, now;        // lane's sequence of the first 64, of the 64 looked at
+  int64_t items, units;      // inclusive sums over the first 64
+  __device__ static SeqWork at(const PagedArgs& a, int i) {
+    return i < a.b.n_seq ? seq_work(a, i) : SeqWork{0, 0, 0, 0, 0, 0, 1};
   }
-  return a.b.n_seq;
-}
+  __device__ void sums(const PagedArgs& a, int64_t* n, int64_t* w) const {
+    *n = wave_scan(now.tiles * a.b.n_kv);
+    *w = wave_scan(now.tiles * a.b.n_kv * now.units);
+  }
+  __device__ explicit Shares(const PagedArgs& a) {
+    first = now = at(a, threadIdx.x & 63);
+    sums(a, &items, &units);
+  }
+  __device__ int64_t total(const PagedArgs& a) {
+    int64_t sum = units, n, w;
+    sum = read_lane(sum, 63);
+    for (int i = 64; i < a.b.n_seq; i += 64) {
+      now = at(a, i + (threadIdx.x & 63));
+      sums(a, &n, &w);
+      sum += read_lane(w, 63);
+    }
+    return sum;
+  }
+  // The sequence that holds item (by_item) or unit number `x`: its work, and the items and units before
+  // it.  n_seq when there is none.
+  __device__ int find(const PagedArgs& a, bool by_item, int64_t x, SeqWork* s, int64_t* items0, int64_t* units0) {
+    int64_t n = items, w = units, n0 = 0, w0 = 0;
+    now = first;
+    for (int i = 0;;) {
+      const uint64_t hit = __ballot((by_item ? n0 + n : w0 + w) > x);
+      if (hit != 0) {
+        const int l = __builtin_ctzll(hit);
+        *s = SeqWork{read_lane(now.row0, l), read_lane(now.pos0, l), read_lane(now.tiles, l), read_lane(now.rows, l),
+                     read_lane(now.lo, l),   read_lane(now.hi, l),   read_lane(now.units, l)};
+        *items0 = n0 + read_lane(n, l) - s->tiles * a.b.n_kv;
+        *units0 = w0 + read_lane(w, l) - s->tiles * a.b.n_kv * s->units;
+        return i + l;
+      }
+      n0 += read_lane(n, 63), w0 += read_lane(w, 63);
+      i += 64;
+      if (i >= a.b.n_seq) return a.b.n_seq;
+      now = at(a, i + (threadIdx.x & 63));
+      sums(a, &n, &w);
+    }
+  }
+};
 
 // `total` units cut into n ranges that differ by at most one unit.
 struct Ranges {
@@ -269,36 +285,60 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
   const bool split = a.tasks != nullptr;
 
   int64_t at, end, items0, units0;
-  int seq;
-  const Ranges ranges(split ? total_units(a) : 1, a.n_wg);
+  Shares shares(a);
+  SeqWork s;
+  const Ranges ranges(split ? shares.total(a) : 1, a.n_wg);
   if (split) {
     if (threadIdx.x == 0) a.tasks[blockIdx.x].parts = 0;
     if (blockIdx.x >= ranges.n) return;
     at = ranges.begin(blockIdx.x), end = ranges.begin(blockIdx.x + 1);
-    seq = find_seq(a, false, at, &items0, &units0);
   } else {
-    seq = find_seq(a, true, blockIdx.x, &items0, &units0);
-    if (seq < b.n_seq) {
-      const SeqWork s = seq_work(a, seq);
-      at = units0 + (blockIdx.x - items0) * s.units, end = at + s.units;
-    }
+    at = blockIdx.x;
   }
+  int seq = shares.find(a, !split, at, &s, &items0, &units0);
   if (seq >= b.n_seq) return;
+  if (!split) at = units0 + (blockIdx.x - items0) * s.units, end = at + s.units;
   const int64_t begin = at;
   while (at < end) {
-    SeqWork s = seq_work(a, seq);
     const int64_t mine = s.tiles * b.n_kv * s.units;
     if (at >= units0 + mine) {  // the next sequence (empty ones have no units)
       units0 += mine;
       if (++seq >= b.n_seq) return;
+      s = seq_work(a, seq);
       continue;
     }
     const int64_t item = first_lane(divide(at - units0, s.units));
     const int u0 = __builtin_amdgcn_readfirstlane(static_cast<int>(at - units0 - item * s.units));
     const int u1 = static_cast<int>(end - at < s.units - u0 ? u0 + (end - at) : s.units);
+    // the range that holds the item's first step (or its last unit, when it has no steps) has its first part
+    const int own = s.units > kFixedUnits ? kFixedUnits : kFixedUnits - 1;
+    if (u1 <= own) {
+      at += u1 - u0;
+      continue;
+    }
     const int kv = __builtin_amdgcn_readfirstlane(static_cast<int>(divide(item, s.tiles)));
     const int64_t tile = first_lane(item - kv * s.tiles);
-    const int k0 = u0 > 0 ? u0 - 1 : 0, k1 = u1 - 1;  // steps
+    const int k0 = u0 > kFixedUnits ? u0 - kFixedUnits : 0, k1 = u1 - kFixedUnits;  // steps
+
+    // the lane's column: its row's visible positions, its query
+    const int64_t cat = tile * kCols + col;
+    const int64_t n_cols = static_cast<int64_t>(s.rows) * a.group;
+    const bool real = cat < n_cols;
+    const int64_t row = real ? divide(cat, a.group) : 0;
+    const int64_t pos = s.pos0 + row;
+    const int hi_q = static_cast<int>(pos < s.hi ? pos : s.hi - 1);
+    const int lo_q = a.window > 0 && pos - a.window + 1 > 0 ? static_cast<int>(pos - a.window + 1) : 0;
+    constexpr int kRaw = 8 * sizeof(T) / 16;
+    uint4v raw[NB][kRaw];
+    {
+      const T* p = static_cast<const T*>(a.q) + (s.row0 + row) * a.q_stride +
+                   (static_cast<int64_t>(kv) * a.group + (real ? cat - row * a.group : 0)) * D + 8 * g;
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+#pragma unroll
+        for (int i = 0; i < kRaw; ++i) raw[blk][i] = reinterpret_cast<const uint4v*>(p + 32 * blk)[i];
+      }
+    }
 
     // this wavefront's tiles: t0 + n * kStep
     const int t0 = s.lo + k0 * kStep + wave * kTile;
@@ -353,23 +393,16 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
     constexpr int kFetch = 2 * ((D <= 64 ? 1 : (D / 2 + 63) / 64 * 2) + 1);
     if (n_tiles > 0) fetch(0);
 
-    // the lane's column: its row's visible positions, its query normalised to 2^14 <= max < 2^15
-    const int64_t cat = tile * kCols + col;
-    const int64_t n_cols = static_cast<int64_t>(s.rows) * a.group;
-    const bool real = cat < n_cols;
-    const int64_t row = real ? divide(cat, a.group) : 0;
-    const int64_t pos = s.pos0 + row;
-    const int hi_q = static_cast<int>(pos < s.hi ? pos : s.hi - 1);
-    const int lo_q = a.window > 0 && pos - a.window + 1 > 0 ? static_cast<int>(pos - a.window + 1) : 0;
+    // the query normalised to 2^14 <= max < 2^15; hidden until here, so that nothing waits for it earlier
     half8 qf[P][NB];
     float fac;
     {
-      const T* p = static_cast<const T*>(a.q) + (s.row0 + row) * a.q_stride +
-                   (static_cast<int64_t>(kv) * a.group + (real ? cat - row * a.group : 0)) * D + 8 * g;
       float x[NB][8], top = 0.0f;
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk) {
-        load8(p + 32 * blk, x[blk]);
+#pragma unroll
+        for (int i = 0; i < kRaw; ++i) asm volatile("" : "+v"(raw[blk][i]));
+        load8(reinterpret_cast<const T*>(&raw[blk]), x[blk]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[blk][i]));
       }
@@ -587,14 +620,14 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
       f[w] = __builtin_amdgcn_exp2f(sref[w][lane] - ref);
       l += sl[w][lane] * f[w];
     }
-    const bool whole = u0 == 0 && u1 == s.units;
+    const bool whole = u0 <= own && u1 == s.units;
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     float* part = nullptr;
     if (!whole) {
       const int slot = at == begin ? 0 : 1;
       part = part_at(a, blockIdx.x, slot, D);
       if (wave == 0) part[lane] = ref, part[64 + lane] = l;
-      if (u0 == 0 && threadIdx.x == 0) {
+      if (u0 <= own && threadIdx.x == 0) {
         const int64_t w = ranges.holder(units0 + (item + 1) * s.units - 1);
         a.tasks[blockIdx.x] = JoinTask{s.row0, tile, s.rows, kv, static_cast<int32_t>(w - blockIdx.x + 1), slot};
       }
