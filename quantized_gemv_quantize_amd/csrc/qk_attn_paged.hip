@@ -42,7 +42,7 @@ namespace {
 
 constexpr int kWaves = 4, kTile = 32, kStep = kWaves * kTile, kCols = 16;
 constexpr int kDirectSteps = 8;  // 1024 positions
-constexpr int kFixedUnits = 2;   // an item's start and end cost about as much as 2 of its steps
+constexpr int kFixedUnits = 3;   // an item's start and end cost about as much as 3 of its steps (1 .. 4: 104, 98, 95, 94 us for 64 sequences of 61 .. 8190)
 constexpr int kMinUnits = 3;     // least units of a range
 
 // Workgroups that fit a CU by the registers of a lane (512 to a lane of the SIMD's wavefronts).

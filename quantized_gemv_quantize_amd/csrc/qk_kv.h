@@ -56,18 +56,19 @@ __host__ __device__ constexpr int64_t kv_half_bytes(int64_t page_tokens, int64_t
   return page_tokens * (dim / 2 + dim / 16);
 }
 
-// Sequence of a packed row: the number of cu[1..n_seq] that are <= row.  All 64 lanes of
-// the wavefront call it with the same row; each tests one entry of 64, so the lookup is
-// one load and one ballot up to 64 sequences (a binary search is a chain of 6 loads).
-// n_seq when the row lies behind the last sequence.
-__device__ __forceinline__ int row_seq(const int32_t* cu, int n_seq, int64_t row) {
+// Sequences of packed rows row0 .. row0 + 3: for each the number of cu[1..n_seq] that are <= row, n_seq when it
+// lies behind the last sequence.  All 64 lanes of the wavefront call it with the same row; each tests
+// one entry of 64, so the lookup is one load and four ballots up to 64 sequences (a binary search is a chain
+// of 6 loads).
+__device__ __forceinline__ void row_seq4(const int32_t* cu, int n_seq, int64_t row0, int* seq) {
   const int lane = threadIdx.x & 63;
-  int seq = 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) seq[r] = 0;
   for (int i = 0; i < n_seq; i += 64) {
-    const bool le = i + lane < n_seq && cu[i + lane + 1] <= row;
-    seq += __popcll(__ballot(le));
+    const int64_t end = i + lane < n_seq ? cu[i + lane + 1] : INT64_MAX;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) seq[r] += __popcll(__ballot(end <= row0 + r));
   }
-  return seq;
 }
 
 // Page of `pos` in sequence `seq`, -1 when the position or the table's entry is out of
