@@ -61,11 +61,20 @@ struct Tile {
   }
 };
 
-// Sum of v over the wavefront, and the same as a scalar.
+template <int CTRL>
+__device__ __forceinline__ int dpp_i(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+// Sum and maximum of non-negative v over the wavefront, as scalars.
 __device__ __forceinline__ int wave_total(int v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-  return __builtin_amdgcn_readfirstlane(v);
+  v += dpp_i<0xB1>(v), v += dpp_i<0x4E>(v), v += dpp_i<0x141>(v), v += dpp_i<0x140>(v);
+  return __builtin_amdgcn_readlane(v, 15) + __builtin_amdgcn_readlane(v, 31) + __builtin_amdgcn_readlane(v, 47) +
+         __builtin_amdgcn_readlane(v, 63);
+}
+__device__ __forceinline__ int wave_most(int v) {
+  v = max(v, dpp_i<0xB1>(v)), v = max(v, dpp_i<0x4E>(v)), v = max(v, dpp_i<0x141>(v)), v = max(v, dpp_i<0x140>(v));
+  return max(max(__builtin_amdgcn_readlane(v, 15), __builtin_amdgcn_readlane(v, 31)),
+             max(__builtin_amdgcn_readlane(v, 47), __builtin_amdgcn_readlane(v, 63)));
 }
 
 // Column tiles of sequence i: its rows are kept inside 0 .. n_q.
@@ -80,23 +89,21 @@ __device__ __forceinline__ int tiles_of(const PromptArgs& a, int i, int cols) {
 // sequence, last first: a later tile sees more keys, and the longest work is not to start last.
 __device__ __forceinline__ bool find_tile(const PromptArgs& a, int cols, int t, int* seq, int* tile) {
   const int lane = threadIdx.x & 63, n_seq = a.b.n_seq;
-  auto count = [&](int level) {  // tiles at place `level` and later
-    int n = 0;
-    for (int i = lane; i < n_seq; i += 64) {
-      const int m = tiles_of(a, i, cols) - level;
-      n += m > 0 ? m : 0;
-    }
-    return wave_total(n);
-  };
-  if (count(0) <= t) return false;
-  int most = 0;
-  for (int i = lane; i < n_seq; i += 64) most = max(most, tiles_of(a, i, cols));
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) most = max(most, __shfl_xor(most, d));
-  // count falls with the level: the last level at which it is above t
-  int lo = 0, hi = __builtin_amdgcn_readfirstlane(most), after = 0;  // count(lo) > t >= count(hi) = after
+  const int mine = lane < n_seq ? tiles_of(a, lane, cols) : 0;  // the first 64 sequences stay in registers
+  auto tiles = [&](int i) { return i == 0 ? mine : (i + lane < n_seq ? tiles_of(a, i + lane, cols) : 0); };
+  int most = 0, all = 0;
+  for (int i = 0; i < n_seq; i += 64) {
+    const int n = tiles(i);
+    most = max(most, n), all += n;
+  }
+  if (wave_total(all) <= t) return false;
+  // tiles at place `level` and later fall with the level: the last level at which they are more than t
+  int lo = 0, hi = wave_most(most), after = 0;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2, n = count(mid);
+    const int mid = (lo + hi) / 2;
+    int n = 0;
+    for (int i = 0; i < n_seq; i += 64) n += max(tiles(i) - mid, 0);
+    n = wave_total(n);
     if (n > t) {
       lo = mid;
     } else {
@@ -105,7 +112,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int cols, int t, 
   }
   int k = t - after;  // the k-th sequence with a tile at place lo
   for (int i = 0; i < n_seq; i += 64) {
-    const uint64_t has = __ballot(i + lane < n_seq && tiles_of(a, i + lane, cols) > lo);
+    const uint64_t has = __ballot(tiles(i) > lo);
     const int n = __popcll(has);
     if (k < n) {
       const uint64_t below = has & ((uint64_t(1) << lane) - 1);
@@ -147,7 +154,7 @@ __device__ __forceinline__ void column_by_keys(const T* q, const T* k, const T* 
 }
 
 template <typename T, int D, int W>
-__global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void attn_prompt_kernel(PromptArgs a) {
   using L = Tile<T, D>;
   constexpr bool kF32T = std::is_same_v<T, float>;
   constexpr int KT = L::kKeys, U = KT / 32, ND = D / 32;
@@ -391,10 +398,9 @@ hipError_t run(const PromptArgs& a, hipStream_t s) {
 
 template <typename T, int D>
 hipError_t prompt_w(const PromptArgs& a, hipStream_t s) {
-  // wavefronts of a workgroup: few workgroups are better small
-  const int64_t cols = a.b.n_q * a.b.n_heads;
-  constexpr int kWide = D <= 128 ? (D == 96 ? 4 : 8) : 4;
-  return cols >= 256 * kCols * kWide ? run<T, D, kWide>(a, s) : run<T, D, 2>(a, s);
+  // Wavefronts of a workgroup.  4 and 8 are alike where there is work for all (550 and 560 us for 8192 rows of 32 / 8
+  // heads of 128 f16), f32 has less LDS left and is better with 4 (160, 192 us); few rows fill more CUs with 2.
+  return a.b.n_q * a.b.n_heads >= 256 * kCols * 4 ? run<T, D, 4>(a, s) : run<T, D, 2>(a, s);
 }
 
 template <typename T>
