@@ -17,15 +17,15 @@
 // dword (lane % 4, block) of each position, one byte permute to a pair of positions.
 //
 // p = 2^(s - ref) with ref = m + E: m is a running maximum that moves only when a score passes it by
-// more than 8 (so no cross-lane maximum in most tiles).  E is 0 for f32, else the power of two that
-// keeps w inside f16 for the value scales met so far, so that small value scales lose no bits.
+// more than kPast (so no cross-lane maximum in most tiles), E the power of two that keeps w inside f16 for
+// the value scales met so far, so that small value scales lose no bits.
 //
 // The score product is the same for every type: q is normalised to a power of two (bf16 then fits
-// f16) and f32 split into two f16 pieces, 22 bits.  In the output product f32 weights stay f32
-// (mfma_16x16x4_f32), f16 weights are rounded to f16, and so are those of bf16 unless the tile has one
-// so small that f16 would leave it less than bf16's 8 bits: weights 2^-32 and less of the largest are
-// all there is of a dim whose other values are 0.  Such a tile (and one with a mask or a scale of 0) is taken
-// in bf16, where turning the codes into bf16 costs 96 of some 400 vector instructions a tile.
+// f16) and f32 split into two f16 pieces, 22 bits.  In the output product weights are f16, two pieces of
+// it for f32, unless a tile of bf16 or f32 has one so small that this would leave it less than the
+// type's precision: weights 2^-32 and less of the largest are all there is of a dim whose other values are
+// 0.  Such a tile (and one with a mask or a scale of 0) is taken in bf16 or f32: turning the codes into bf16
+// costs 96 of some 400 vector instructions a tile, f32 products 8 times the matrix time.
 //
 // Work is split over the positions when the table allows more than kDirectSteps steps: all
 // items' steps laid end to end are cut into equal ranges, one a workgroup, however uneven
@@ -269,7 +269,10 @@ template <typename T, int D>
 __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(PagedArgs a) {
   constexpr int NB = D / 32, kRegs = NB * 2;  // float4 registers of the output
   constexpr bool kF32T = std::is_same_v<T, float>, kBf16T = std::is_same_v<T, bf16>;
-  constexpr int P = kF32T ? 2 : 1;  // f16 pieces of a query
+  constexpr int P = kF32T ? 2 : 1;  // f16 pieces of a query and of a weight
+  // how far (log2) a score may pass the maximum before that moves; the least weight that f16 pieces hold to
+  // the type's precision: 2 pieces to 2^-21 (the second's last place is 2^-24), 8 bits for bf16; f16 is what it is
+  constexpr float kPast = kF32T ? 2.0f : 8.0f, kLeast = kF32T ? 0x1p-4f : (kBf16T ? 0x1p-17f : 0.0f);
   // A wavefront's LDS: two tiles on their way from memory (each two halves of K codes, V codes, K
   // scales, V scales), and in the same place its output registers for the joining of the four.
   constexpr int kHalfBytes = 18 * D, kTileBytes = 2 * kHalfBytes, kWaveBytes = 2 * kTileBytes;
@@ -456,7 +459,7 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         lds_dwords<2 * NB>(in + h * kHalfBytes + 16 * D + 32 * NB + d_lane, dv[h]);
-        if constexpr (!kF32T) lds_dwords<1>(in + h * kHalfBytes + 16 * D + 32 * NB + lane % (8 * NB) * 4, &dt[h]);
+        lds_dwords<1>(in + h * kHalfBytes + 16 * D + 32 * NB + lane % (8 * NB) * 4, &dt[h]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) lds_dwords<NB>(in + h * kHalfBytes + 8 * D + v_lane + i * (D / 2), vc[h][i]);
       }
@@ -490,31 +493,26 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
             see[i] = p <= hi_q && p >= lo_q && !bad[h];
             if (!see[i]) sc[h][i] = -INFINITY;
           }
-          if constexpr (!kF32T) {
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k)
-              dtop = largest_half(dv[h][k] & ((see[2 * k / NB] ? 0xFFFFu : 0u) | (see[(2 * k + 1) / NB] ? 0xFFFF0000u : 0u)), dtop);
-          }
+          for (int k = 0; k < 2 * NB; ++k)
+            dtop = largest_half(dv[h][k] & ((see[2 * k / NB] ? 0xFFFFu : 0u) | (see[(2 * k + 1) / NB] ? 0xFFFF0000u : 0u)), dtop);
         }
-      } else if constexpr (!kF32T) {
+      } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) dtop = largest_half(dt[h], dtop);  // every value scale of the half once
       }
       float top = sc[0][0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[i / 4][i % 4]);
-      if (__any(top > st.lim || (!kF32T && dtop > st.dlim))) {
+      if (__any(top > st.lim || dtop > st.dlim)) {
         top = rows_max(top);
         st.m = fmaxf(st.m, top);
-        st.lim = st.m + 8.0f;
-        float ref = st.m;
-        if constexpr (!kF32T) {
-          const uint32_t dm = static_cast<uint32_t>(wave_max(static_cast<float>(dtop)));
-          st.e16 = max(st.e16, dm >> 10);
-          st.dlim = (st.e16 + 2) << 10;
-          // scales below 2^(e16 - 14), weights below 2^6 now and 2^15 until either limit is passed
-          ref += static_cast<float>(static_cast<int>(st.e16)) - 20.0f;
-        }
+        st.lim = st.m + kPast;
+        const uint32_t dm = static_cast<uint32_t>(wave_max(static_cast<float>(dtop)));
+        st.e16 = max(st.e16, dm >> 10);
+        st.dlim = (st.e16 + 2) << 10;
+        // scales are below 2^(e16 - 14), weights below 2^(14 - kPast), until a limit is passed below 2^15
+        const float ref = st.m + (static_cast<float>(static_cast<int>(st.e16)) - (28.0f - kPast));
         const float keep = __builtin_amdgcn_exp2f(st.ref - ref);
         st.ref = ref;
         st.l *= keep;
@@ -542,65 +540,64 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
           v1[k] = high_nibbles(x);
         }
       };
-      if constexpr (kF32T) {
+      half8 wf[P][NB];
+      float least = FLT_MAX;
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = weight(i, blk);
+        if constexpr (kLeast > 0.0f) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) least = fminf(least, fabsf(w[i]));
+        }
+        wf[0][blk] = pack8(w);
+        if constexpr (P == 2) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] -= static_cast<float>(wf[0][blk][i]);
+          wf[1][blk] = pack8(w);
+        }
+      }
+      if (!masked && !__any(least < kLeast)) {
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
           uint32_t v0[4], v1[4];
           codes(blk, v0, v1);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float w = masked_weight(i, blk);
-            st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(half_at(v0, i), w, st.o[blk][0], 0, 0, 0);
-            st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(half_at(v1, i), w, st.o[blk][1], 0, 0, 0);
+          for (int e = P - 1; e >= 0; --e) {
+            st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v0), wf[e][blk], st.o[blk][0], 0, 0, 0);
+            st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v1), wf[e][blk], st.o[blk][1], 0, 0, 0);
           }
         }
       } else {
-        half8 wf[NB];
-        float least = FLT_MAX;
+        // weights once more: hidden, so that they are not kept in registers on the common path for this
+#pragma unroll
+        for (int i = 0; i < 8; ++i) asm("" : "+v"(p[i / 4][i % 4]));
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
           float w[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = weight(i, blk);
-          if constexpr (kBf16T) {
+          for (int i = 0; i < 8; ++i) w[i] = masked_weight(i, blk);
+          uint32_t v0[4], v1[4];
+          codes(blk, v0, v1);
+          if constexpr (kF32T) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) least = fminf(least, fabsf(w[i]));
-          }
-          wf[blk] = pack8(w);
-        }
-        // less than 8 bits left in f16
-        if (!(masked || (kBf16T && __any(least < 0x1p-17f)))) {
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk) {
-            uint32_t v0[4], v1[4];
-            codes(blk, v0, v1);
-            st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v0), wf[blk], st.o[blk][0], 0, 0, 0);
-            st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v1), wf[blk], st.o[blk][1], 0, 0, 0);
-          }
-        } else {
-          // weights once more: hidden, so that they are not kept in registers on the common path for this
-#pragma unroll
-          for (int i = 0; i < 8; ++i) asm("" : "+v"(p[i / 4][i % 4]));
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk) {
-            float w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = masked_weight(i, blk);
-            uint32_t v0[4], v1[4];
-            codes(blk, v0, v1);
-            if constexpr (kBf16T) {
-              bf16x8 wb;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) wb[i] = static_cast<bf16>(w[i]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) v0[k] = half_pair_to_bf16(v0[k]), v1[k] = half_pair_to_bf16(v1[k]);
-              st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<bf16x8>(v0), wb, st.o[blk][0], 0, 0, 0);
-              st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<bf16x8>(v1), wb, st.o[blk][1], 0, 0, 0);
-            } else {
-              const half8 wm = pack8(w);
-              st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v0), wm, st.o[blk][0], 0, 0, 0);
-              st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v1), wm, st.o[blk][1], 0, 0, 0);
+            for (int i = 0; i < 8; ++i) {
+              st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(half_at(v0, i), w[i], st.o[blk][0], 0, 0, 0);
+              st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(half_at(v1, i), w[i], st.o[blk][1], 0, 0, 0);
             }
+          } else if constexpr (kBf16T) {
+            bf16x8 wb;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) wb[i] = static_cast<bf16>(w[i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v0[k] = half_pair_to_bf16(v0[k]), v1[k] = half_pair_to_bf16(v1[k]);
+            st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<bf16x8>(v0), wb, st.o[blk][0], 0, 0, 0);
+            st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<bf16x8>(v1), wb, st.o[blk][1], 0, 0, 0);
+          } else {
+            const half8 wm = pack8(w);
+            st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v0), wm, st.o[blk][0], 0, 0, 0);
+            st.o[blk][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v1), wm, st.o[blk][1], 0, 0, 0);
           }
         }
       }
