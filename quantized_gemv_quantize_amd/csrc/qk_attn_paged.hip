@@ -46,7 +46,7 @@ constexpr int kFixedUnits = 3;   // an item's start and end cost about as much a
 constexpr int kMinUnits = 3;     // least units of a range
 
 // Workgroups that fit a CU by the registers of a lane (512 to a lane of the SIMD's wavefronts).
-constexpr int groups_per_cu(int dim) { return dim <= 64 ? 3 : (dim <= 128 ? 2 : 1); }
+constexpr int groups_per_cu(int dim, bool f32) { return dim > 128 ? 1 : (dim <= 64 ? 4 : 3) - (f32 && dim != 96 ? 1 : 0); }
 
 struct JoinTask;
 struct PagedArgs {
@@ -171,9 +171,9 @@ struct Shares {
 struct Ranges {
   int64_t n, q, r;
   __device__ Ranges(int64_t total, int n_wg) {
-    n = divide(total, kMinUnits);
+    n = first_lane(divide(total, kMinUnits));
     n = n < 1 ? 1 : (n < n_wg ? n : n_wg);
-    q = divide(total, n), r = total - q * n;
+    q = first_lane(divide(total, n)), r = total - q * n;
   }
   __device__ int64_t begin(int64_t w) const { return w * q + (w < r ? w : r); }
   __device__ int64_t holder(int64_t unit) const {
@@ -266,7 +266,7 @@ __device__ __forceinline__ void store_out(const PagedArgs& a, int64_t row0, int 
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(PagedArgs a) {
+__global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) void attn_paged_kernel(PagedArgs a) {
   constexpr int NB = D / 32, kRegs = NB * 2;  // float4 registers of the output
   constexpr bool kF32T = std::is_same_v<T, float>, kBf16T = std::is_same_v<T, bf16>;
   constexpr int P = kF32T ? 2 : 1;  // f16 pieces of a query and of a weight
@@ -425,8 +425,8 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
       }
     }
     // tiles in lo_max .. hi_min + 1 - kTile need no mask
-    const int64_t first = divide(tile * kCols, a.group);
-    const int64_t last = divide((tile + 1) * kCols < n_cols ? (tile + 1) * kCols - 1 : n_cols - 1, a.group);
+    const int64_t first = first_lane(divide(tile * kCols, a.group));
+    const int64_t last = first_lane(divide((tile + 1) * kCols < n_cols ? (tile + 1) * kCols - 1 : n_cols - 1, a.group));
     const int64_t hi_min = s.pos0 + first < s.hi ? s.pos0 + first : s.hi - 1;
     const int64_t lo_max = a.window > 0 ? s.pos0 + last - a.window + 1 : 0;
 
@@ -449,37 +449,32 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
         wait_loads<0>();
       }
       const uint8_t* const in = ring + (n & 1) * kTileBytes;
-      // all of the tile's LDS reads at once: they are what the wavefront waits for
-      uint32_t kc[2][NB], dk[2][2 * NB], dv[2][2 * NB], vc[2][4][NB], dt[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        lds_dwords<NB>(in + h * kHalfBytes + k_lane, kc[h]);
-        lds_dwords<2 * NB>(in + h * kHalfBytes + 16 * D + d_lane, dk[h]);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        lds_dwords<2 * NB>(in + h * kHalfBytes + 16 * D + 32 * NB + d_lane, dv[h]);
-        lds_dwords<1>(in + h * kHalfBytes + 16 * D + 32 * NB + lane % (8 * NB) * 4, &dt[h]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lds_dwords<NB>(in + h * kHalfBytes + 8 * D + v_lane + i * (D / 2), vc[h][i]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+      uint32_t dv[2][2 * NB], dt[2];
       float sc[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[h][i] = 0.0f;
+        uint32_t kc[NB], dk[2 * NB];
+        lds_dwords<NB>(in + h * kHalfBytes + k_lane, kc);
+        lds_dwords<2 * NB>(in + h * kHalfBytes + 16 * D + d_lane, dk);
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
-          const half8 kf = nibbles_to_f16(kc[h][blk]);
+          const half8 kf = nibbles_to_f16(kc[blk]);
           float4v c = {0, 0, 0, 0};
           if constexpr (P == 2) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[1][blk], c, 0, 0, 0);
           c = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[0][blk], c, 0, 0, 0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[h][i] = fmaf(c[i], half_at(dk[h], i * NB + blk), sc[h][i]);
+          for (int i = 0; i < 4; ++i) sc[h][i] = fmaf(c[i], half_at(dk, i * NB + blk), sc[h][i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[h][i] *= fac;
+        __builtin_amdgcn_sched_barrier(0);  // one half's products at a time in registers
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        lds_dwords<2 * NB>(in + h * kHalfBytes + 16 * D + 32 * NB + d_lane, dv[h]);
+        lds_dwords<1>(in + h * kHalfBytes + 16 * D + 32 * NB + lane % (8 * NB) * 4, &dt[h]);
       }
       uint32_t dtop = 0;
       const bool masked = t < lo_max || t + kTile > hi_min + 1 || bad[0] || bad[1];
@@ -528,14 +523,12 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
           st.l += p[h][i];
         }
       }
-      // + 0: a multiply-add takes the f16 as it is (v_fma_mix_f32).  What a masked slot holds is not to be
-      // multiplied, not even by 0: it may be infinite or NaN.
-      auto weight = [&](int i, int blk) { return fmaf(p[i / 4][i % 4], half_at(dv[i / 4], i % 4 * NB + blk), 0.0f); };
-      auto masked_weight = [&](int i, int blk) { return p[i / 4][i % 4] == 0.0f ? 0.0f : weight(i, blk); };
-      auto codes = [&](int blk, uint32_t (&v0)[4], uint32_t (&v1)[4]) {
+      // + 0: a multiply-add takes the f16 as it is (v_fma_mix_f32)
+      auto weight = [&](int i, float d) { return fmaf(p[i / 4][i % 4], d, 0.0f); };
+      auto codes = [&](const uint32_t (&w)[2][4], uint32_t (&v0)[4], uint32_t (&v1)[4]) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t x = __builtin_amdgcn_perm(vc[k / 2][k % 2 * 2 + 1][blk], vc[k / 2][k % 2 * 2][blk], sel);
+          const uint32_t x = __builtin_amdgcn_perm(w[k / 2][k % 2 * 2 + 1], w[k / 2][k % 2 * 2], sel);
           v0[k] = low_nibbles(x);
           v1[k] = high_nibbles(x);
         }
@@ -546,7 +539,7 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
       for (int blk = 0; blk < NB; ++blk) {
         float w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = weight(i, blk);
+        for (int i = 0; i < 8; ++i) w[i] = weight(i, half_at(dv[i / 4], i % 4 * NB + blk));
         if constexpr (kLeast > 0.0f) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) least = fminf(least, fabsf(w[i]));
@@ -559,10 +552,18 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
         }
       }
       if (!masked && !__any(least < kLeast)) {
+        uint32_t vc[2][4][NB];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) lds_dwords<NB>(in + h * kHalfBytes + 8 * D + v_lane + i * (D / 2), vc[h][i]);
+        }
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
-          uint32_t v0[4], v1[4];
-          codes(blk, v0, v1);
+          uint32_t w[2][4], v0[4], v1[4];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i / 4][i % 4] = vc[i / 4][i % 4][blk];
+          codes(w, v0, v1);
 #pragma unroll
           for (int e = P - 1; e >= 0; --e) {
             st.o[blk][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand<half8>(v0), wf[e][blk], st.o[blk][0], 0, 0, 0);
@@ -570,16 +571,22 @@ __global__ __launch_bounds__(256, groups_per_cu(D)) void attn_paged_kernel(Paged
           }
         }
       } else {
-        // weights once more: hidden, so that they are not kept in registers on the common path for this
+        // scales and codes are read from LDS once more, a block at a time, so that this branch keeps no registers
 #pragma unroll
-        for (int i = 0; i < 8; ++i) asm("" : "+v"(p[i / 4][i % 4]));
+        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(p[i / 4][i % 4])::"memory");
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
           float w[8];
+          uint32_t c[2][4], v0[4], v1[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = masked_weight(i, blk);
-          uint32_t v0[4], v1[4];
-          codes(blk, v0, v1);
+          for (int i = 0; i < 8; ++i) {
+            const uint8_t* const from = in + i / 4 * kHalfBytes;
+            const uint16_t d = *reinterpret_cast<const uint16_t*>(from + 16 * D + 32 * NB + d_lane + (i % 4 * NB + blk) * 2);
+            // what a masked slot holds is not to be multiplied, not even by 0: it may be infinite or NaN
+            w[i] = p[i / 4][i % 4] == 0.0f ? 0.0f : weight(i, f16_to_f32(d));
+            lds_dwords<1>(from + 8 * D + v_lane + i % 4 * (D / 2) + blk * 4, &c[i / 4][i % 4]);
+          }
+          codes(c, v0, v1);
           if constexpr (kF32T) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -698,7 +705,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(PagedArgs a) {
 }
 
 // Workgroups of the split form: as many as run at once.
-int split_groups(int dim) { return 256 * groups_per_cu(dim); }
+int split_groups(int dim, bool f32) { return 256 * groups_per_cu(dim, f32); }
 
 // Most items a batch can have: every row with its group's heads, and a part-filled item to a sequence.
 int64_t max_items(const KvBatch& b, int n_heads) {
@@ -736,13 +743,13 @@ hipError_t paged_t(const PagedArgs& a, int dim, hipStream_t s) {
 }  // namespace
 
 int64_t attn_paged_ws_bytes(const KvBatch& b, int dim, int) {
-  return is_split(b) ? split_groups(dim) * static_cast<int64_t>(sizeof(JoinTask) + 2 * part_floats(dim) * sizeof(float)) : 0;
+  return is_split(b) ? split_groups(dim, false) * static_cast<int64_t>(sizeof(JoinTask) + 2 * part_floats(dim) * sizeof(float)) : 0;
 }
 
 hipError_t launch_attn_paged(const KvBatch& b, int dim, int dtype, const uint8_t* pages, const void* q, int64_t q_stride,
                              int n_heads, float scale, int64_t window, void* out, void* ws, hipStream_t s) {
   const PagedArgs a{b, pages, q, out, is_split(b) ? static_cast<JoinTask*>(ws) : nullptr, q_stride, window, n_heads,
-                    n_heads / b.n_kv, split_groups(dim), scale};
+                    n_heads / b.n_kv, split_groups(dim, dtype == kF32), scale};
   switch (dtype) {
     case kF32: return paged_t<float>(a, dim, s);
     case kF16: return paged_t<_Float16>(a, dim, s);
