@@ -24,7 +24,7 @@
 // f16) and f32 split into two f16 pieces, 22 bits.  In the output product weights are f16, two pieces of
 // it for f32, unless a tile of bf16 or f32 has one so small that this would leave it less than the
 // type's precision: weights 2^-32 and less of the largest are all there is of a dim whose other values are
-// 0.  Such a tile (and one with a mask or a scale of 0) is taken in bf16 or f32: turning the codes into bf16
+// 0.  Such a tile (and one with a scale of 0, or a mask over an infinite or NaN scale) is taken in bf16 or f32: turning the codes into bf16
 // costs 96 of some 400 vector instructions a tile, f32 products 8 times the matrix time.
 //
 // Work is split over the positions when the table allows more than kDirectSteps steps: all
@@ -95,10 +95,10 @@ __device__ __forceinline__ SeqWork seq_work(const PagedArgs& a, int64_t i) {
   return s;
 }
 
-__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+// Inclusive sums over the first n lanes.
+__device__ __forceinline__ int64_t wave_scan(int64_t v, int n) {
   const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
+  for (int d = 1; d < n; d *= 2) {
     const int64_t o = __shfl_up(v, d);
     if (lane >= d) v += o;
   }
@@ -125,21 +125,22 @@ struct Shares {
   __device__ static SeqWork at(const PagedArgs& a, int i) {
     return i < a.b.n_seq ? seq_work(a, i) : SeqWork{0, 0, 0, 0, 0, 0, 1};
   }
-  __device__ void sums(const PagedArgs& a, int64_t* n, int64_t* w) const {
-    *n = wave_scan(now.tiles * a.b.n_kv);
-    *w = wave_scan(now.tiles * a.b.n_kv * now.units);
+  __device__ static int lanes(const PagedArgs& a, int i) { return a.b.n_seq - i < 64 ? a.b.n_seq - i : 64; }
+  __device__ void sums(const PagedArgs& a, int i, int64_t* n, int64_t* w) const {
+    *n = wave_scan(now.tiles * a.b.n_kv, lanes(a, i));
+    *w = wave_scan(now.tiles * a.b.n_kv * now.units, lanes(a, i));
   }
   __device__ explicit Shares(const PagedArgs& a) {
     first = now = at(a, threadIdx.x & 63);
-    sums(a, &items, &units);
+    sums(a, 0, &items, &units);
   }
   __device__ int64_t total(const PagedArgs& a) {
-    int64_t sum = units, n, w;
-    sum = read_lane(sum, 63);
+    if (a.b.n_seq == 0) return 0;
+    int64_t sum = read_lane(units, lanes(a, 0) - 1), n, w;
     for (int i = 64; i < a.b.n_seq; i += 64) {
       now = at(a, i + (threadIdx.x & 63));
-      sums(a, &n, &w);
-      sum += read_lane(w, 63);
+      sums(a, i, &n, &w);
+      sum += read_lane(w, lanes(a, i) - 1);
     }
     return sum;
   }
@@ -149,7 +150,7 @@ struct Shares {
     int64_t n = items, w = units, n0 = 0, w0 = 0;
     now = first;
     for (int i = 0;;) {
-      const uint64_t hit = __ballot((by_item ? n0 + n : w0 + w) > x);
+      const uint64_t hit = __ballot(static_cast<int>(threadIdx.x & 63) < lanes(a, i) && (by_item ? n0 + n : w0 + w) > x);
       if (hit != 0) {
         const int l = __builtin_ctzll(hit);
         *s = SeqWork{read_lane(now.row0, l), read_lane(now.pos0, l), read_lane(now.tiles, l), read_lane(now.rows, l),
@@ -158,11 +159,11 @@ struct Shares {
         *units0 = w0 + read_lane(w, l) - s->tiles * a.b.n_kv * s->units;
         return i + l;
       }
+      if (i + 64 >= a.b.n_seq) return a.b.n_seq;
       n0 += read_lane(n, 63), w0 += read_lane(w, 63);
       i += 64;
-      if (i >= a.b.n_seq) return a.b.n_seq;
       now = at(a, i + (threadIdx.x & 63));
-      sums(a, &n, &w);
+      sums(a, i, &n, &w);
     }
   }
 };
@@ -238,6 +239,20 @@ __device__ __forceinline__ half8 pack8(const float* v) {
   return h;
 }
 
+// A SIMD issues from its oldest wavefront first, so equal ranges end far apart and the last run alone.  The
+// further a wavefront is in its range, the lower its priority: those that lag catch up.
+__device__ __forceinline__ void set_priority(int done, int quarter) {
+  if (done < quarter) {
+    __builtin_amdgcn_s_setprio(3);
+  } else if (done < 2 * quarter) {
+    __builtin_amdgcn_s_setprio(2);
+  } else if (done < 3 * quarter) {
+    __builtin_amdgcn_s_setprio(1);
+  } else {
+    __builtin_amdgcn_s_setprio(0);
+  }
+}
+
 // The running softmax of one wavefront: lane's column is lane % 16.
 template <int NB>
 struct State {
@@ -302,6 +317,7 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
   if (seq >= b.n_seq) return;
   if (!split) at = units0 + (blockIdx.x - items0) * s.units, end = at + s.units;
   const int64_t begin = at;
+  const int quarter = static_cast<int>(end - begin < (1 << 29) ? (end - begin) / 4 + 1 : 1 << 27);
   while (at < end) {
     const int64_t mine = s.tiles * b.n_kv * s.units;
     if (at >= units0 + mine) {  // the next sequence (empty ones have no units)
@@ -323,6 +339,21 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
     const int64_t tile = first_lane(item - kv * s.tiles);
     const int k0 = u0 > kFixedUnits ? u0 - kFixedUnits : 0, k1 = u1 - kFixedUnits;  // steps
 
+    // this wavefront's tiles: t0 + n * kStep
+    const int t0 = s.lo + k0 * kStep + wave * kTile;
+    const int64_t stop = static_cast<int64_t>(s.lo) + static_cast<int64_t>(k1) * kStep;
+    const int t_end = stop < s.hi ? static_cast<int>(stop) : s.hi;
+    const int n_tiles = t0 < t_end ? (t_end - t0 - 1) / kStep + 1 : 0;
+    // pages of the 16-position halves of tiles n & ~31 .., one a lane
+    const int32_t* table = b.table + static_cast<int64_t>(seq) * b.max_pages;
+    auto pages_from = [&](int n) {
+      const int64_t p = t0 + static_cast<int64_t>(n + lane / 2) * kStep + (lane & 1) * 16;
+      int page = -1;
+      if (p < s.hi) page = table[p >> b.page_shift];
+      return page;
+    };
+    int page_vec = pages_from(0);  // on its way before the queries
+
     // the lane's column: its row's visible positions, its query
     const int64_t cat = tile * kCols + col;
     const int64_t n_cols = static_cast<int64_t>(s.rows) * a.group;
@@ -343,33 +374,19 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
       }
     }
 
-    // this wavefront's tiles: t0 + n * kStep
-    const int t0 = s.lo + k0 * kStep + wave * kTile;
-    const int64_t stop = static_cast<int64_t>(s.lo) + static_cast<int64_t>(k1) * kStep;
-    const int t_end = stop < s.hi ? static_cast<int>(stop) : s.hi;
-    const int n_tiles = t0 < t_end ? (t_end - t0 - 1) / kStep + 1 : 0;
-    int page_vec = -1;  // pages of the 16-position halves of tiles n & ~31 ..
-    const int32_t* table = b.table + static_cast<int64_t>(seq) * b.max_pages;
     const int mask = static_cast<int>(tokens) - 1;
     const int v_at = static_cast<int>(half), scales_at = static_cast<int>(tokens) * (D / 2);
     bool bad[2], bad_next[2];
     // Starts the loads of tile n into its place of the ring.
     auto fetch = [&](int n) {
-      if ((n & 31) == 0) {
-        const int64_t p = t0 + static_cast<int64_t>(n + lane / 2) * kStep + (lane & 1) * 16;
-        page_vec = -1;
-        if (p < s.hi) {
-          const int32_t page = table[p >> b.page_shift];
-          if (page >= 0 && page < b.n_pages) page_vec = page;
-        }
-      }
+      if ((n & 31) == 0 && n > 0) page_vec = pages_from(n);
       // the LDS this writes was read by the tile before last: those reads have to be back
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int page = __builtin_amdgcn_readlane(page_vec, 2 * (n & 31) + h);
-        bad_next[h] = page < 0;  // page 0 is read in its place, and masked
-        uint8_t* p = const_cast<uint8_t*>(a.pages) + (static_cast<int64_t>(page < 0 ? 0 : page) * b.n_kv + kv) * 2 * half;
+        bad_next[h] = page < 0 || page >= b.n_pages;  // page 0 is read in its place, and masked
+        uint8_t* p = const_cast<uint8_t*>(a.pages) + (static_cast<int64_t>(bad_next[h] ? 0 : page) * b.n_kv + kv) * 2 * half;
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(p, 0, static_cast<int>(2 * half), 0x00027000);
         const int slot = (t0 + n * kStep + 16 * h) & mask;
         uint8_t* to = ring + (n & 1) * kTileBytes + h * kHalfBytes;
@@ -436,11 +453,13 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
 #pragma unroll
     for (int i = 0; i < NB; ++i) st.o[i][0] = st.o[i][1] = float4v{0, 0, 0, 0};
 
+    const int done = static_cast<int>(at - begin < (1 << 29) ? at - begin : 1 << 29);
     // lane offsets in a half: its row of K codes, its 4 positions' scales, its dwords of the first of its 4 V rows
     const int k_lane = col * (D / 2) + g * NB * 4, d_lane = 4 * g * NB * 2, v_lane = 4 * g * (D / 2) + (col % 4) * NB * 4;
     const uint32_t sel = (col / 4) | 0x0C000C00u | (4 + col / 4) << 16;  // byte m of two dwords, each in a 16-bit half
     for (int n = 0; n < n_tiles; ++n) {
       const int t = t0 + n * kStep;
+      set_priority(done + n, quarter);
       bad[0] = bad_next[0], bad[1] = bad_next[1];
       if (n + 1 < n_tiles) {
         fetch(n + 1);
@@ -478,7 +497,9 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
       }
       uint32_t dtop = 0;
       const bool masked = t < lo_max || t + kTile > hi_min + 1 || bad[0] || bad[1];
+      bool odd = false;  // a masked slot may hold a scale that is not to be multiplied, not even by 0
       if (masked) {
+        odd = __any(max(largest_half(dt[0], 0), largest_half(dt[1], 0)) >= 0x7C00u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           bool see[4];
@@ -551,7 +572,18 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
           wf[1][blk] = pack8(w);
         }
       }
-      if (!masked && !__any(least < kLeast)) {
+      if (kLeast > 0.0f && masked) {  // the zeros of a mask are no small weights
+        least = FLT_MAX;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float w = fabsf(weight(i, half_at(dv[i / 4], i % 4 * NB + blk)));
+            least = w > 0.0f ? fminf(least, w) : least;
+          }
+        }
+      }
+      if (!odd && !__any(least < kLeast)) {
         uint32_t vc[2][4][NB];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -582,7 +614,6 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
           for (int i = 0; i < 8; ++i) {
             const uint8_t* const from = in + i / 4 * kHalfBytes;
             const uint16_t d = *reinterpret_cast<const uint16_t*>(from + 16 * D + 32 * NB + d_lane + (i % 4 * NB + blk) * 2);
-            // what a masked slot holds is not to be multiplied, not even by 0: it may be infinite or NaN
             w[i] = p[i / 4][i % 4] == 0.0f ? 0.0f : weight(i, f16_to_f32(d));
             lds_dwords<1>(from + 8 * D + v_lane + i % 4 * (D / 2) + blk * 4, &c[i / 4][i % 4]);
           }
