@@ -14,7 +14,12 @@
 // operand (several keys of one dim) is read from LDS by the transposing load.
 //
 // p = 2^(c S - m): m is a running maximum that moves only when a score passes it by more than 8, so
-// most tiles need no maximum across lanes and no rescaling.  f32 runs on mfma_32x32x2_f32 throughout.
+// most tiles need no maximum across lanes and no rescaling.
+//
+// f32: every operand (q, k, v, p) is split into three bf16 pieces of 8 bits, which keep f32's range, and a
+// product is the six products of pieces that matter (the rest is below 2^-24 of it): 6/16 of the
+// matrix time of mfma_32x32x2_f32.  Keys and values come through registers, are split once for the
+// workgroup and stored as three planes.
 //
 // A masked key's weight is 0, but 0 times an infinite or NaN value is NaN: a wavefront whose output is
 // not finite at the end computes its rows again key by key, over the visible keys only.
@@ -31,6 +36,9 @@ typedef float float16v __attribute__((ext_vector_type(16)));
 typedef short short4v __attribute__((ext_vector_type(4)));
 
 constexpr int kCols = 32;
+// Groups of 32 columns below which a group is shared by several wavefronts: with 140 groups of 1500 rows, 300 of 1200
+// and 600 of 600 (D = 128 bf16), 21, 21 and 30 us against 34, 30 and 20 with a wavefront to a group.
+constexpr int64_t kFewGroups = 512;
 
 struct PromptArgs {
   PromptBatch b;
@@ -40,26 +48,42 @@ struct PromptArgs {
   float scale;
 };
 
-// LDS layout of a tile: rows of D elements in 16-byte pieces; piece p of row r lies at place p ^ swizzle(r), which
-// spreads what one load instruction reads over the banks.
-template <typename T, int D>
+// LDS layout of a tile (for f32 of each plane): rows of D 16-bit elements in 16-byte pieces; piece p of row r
+// lies at place p ^ swizzle(r), which spreads what one load instruction reads over the banks.
+template <typename T, int D, int KT>
 struct Tile {
-  static constexpr int kPer = 16 / sizeof(T);             // elements of a piece
-  static constexpr int kPieces = D / kPer;                // of a row
-  static constexpr int kRow = D * sizeof(T);              // bytes
-  static constexpr int kKeys = kRow <= 512 ? 64 : 32;     // two tiles of K and V in 128 KB
-  static constexpr int kBytes = kKeys * kRow;             // K or V
-  static constexpr int kLoads = kBytes / 1024;            // load instructions
-  // K: 32 rows at one piece.  Rows are 256 bytes apart (or 128, 512): 8 rows get 8 places; rows of 192 or 384
+  static constexpr bool kF32 = std::is_same_v<T, float>;
+  static constexpr int kPieces = D / 8;                        // of a row
+  static constexpr int kRow = D * 2;                           // bytes
+  static constexpr int kBytes = KT * kRow;                  // K or V
+  static constexpr int kLoads = kBytes / 1024;                 // load instructions
+  static constexpr int kLds = (kF32 ? 6 : 4) * kBytes;         // f32: 3 planes of K and V, else K, V, K, V
+  // K: 32 rows at one piece.  Rows are 256 bytes apart (or 128, 512): 8 rows get 8 places; rows of 192
   // bytes come in pairs, for which 4 places do.
   __device__ static int k_swizzle(int r) { return D == 96 ? (r >> 1) & 3 : r & 7; }
-  // V: 4 rows at 64 bytes (16 bit), 2 rows 4 apart at 128 bytes (f32)
-  __device__ static int v_swizzle(int r) {
-    if (D == 96) return 0;
-    if (sizeof(T) == 4) return ((r >> 2) & 1) << 3;
-    return D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
-  }
+  // V: 4 rows at 64 bytes
+  __device__ static int v_swizzle(int r) { return D == 96 ? 0 : (D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2); }
 };
+
+// x as three bf16 pieces, each the rounding of what the ones before it leave.
+__device__ __forceinline__ void split8(const float* x, bf16x8* hi, bf16x8* mid, bf16x8* lo) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    (*hi)[i] = static_cast<bf16>(x[i]);
+    const float r = x[i] - static_cast<float>((*hi)[i]);
+    (*mid)[i] = static_cast<bf16>(r);
+    (*lo)[i] = static_cast<bf16>(r - static_cast<float>((*mid)[i]));
+  }
+}
+// c + a b of pieces: the six products above 2^-24, the small ones first.
+__device__ __forceinline__ float16v product6(const bf16x8 (&a)[3], const bf16x8 (&b)[3], float16v c) {
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[2], b[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[0], b[2], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[1], b[1], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[1], b[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[0], b[1], c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[0], b[0], c, 0, 0, 0);
+}
 
 template <int CTRL>
 __device__ __forceinline__ int dpp_i(int v) {
@@ -125,10 +149,10 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int cols, int t, 
   return false;
 }
 
-// One column, key by key.
+// Dims dim0 .. dim0 + n - 1 of one column's output, key by key.
 template <typename T, int D>
 __device__ __forceinline__ void column_by_keys(const T* q, const T* k, const T* v, int64_t k_stride, int64_t v_stride, int64_t lo,
-                                               int64_t hi, float c, T* out) {
+                                               int64_t hi, float c, int dim0, int n, T* out) {
   const int lane = threadIdx.x & 63;
   constexpr int N = (D + 63) / 64;
   float m = -FLT_MAX, l = 0.0f, o[N] = {}, x[N] = {};
@@ -149,24 +173,30 @@ __device__ __forceinline__ void column_by_keys(const T* q, const T* k, const T* 
     }
   }
   for (int i = 0; i < N; ++i) {
-    if (lane + 64 * i < D) out[lane + 64 * i] = static_cast<T>(l != 0.0f ? o[i] / l : 0.0f);
+    const int e = lane + 64 * i;
+    if (e >= dim0 && e < dim0 + n) out[e] = static_cast<T>(l != 0.0f ? o[i] / l : 0.0f);
   }
 }
 
-template <typename T, int D, int W>
+// W wavefronts: W / (S H) groups of 32 columns.  A group is shared by S wavefronts that take 32 keys of a tile of KT each
+// (S = 1: all), or by H that take D / H dims each and add their scores up through LDS.
+template <typename T, int D, int W, int KT, int S, int H>
 __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void attn_prompt_kernel(PromptArgs a) {
-  using L = Tile<T, D>;
+  using L = Tile<T, D, KT>;
+  static_assert((S == 1 || KT == 32 * S) && (H == 1 || (S == 1 && KT == 32)));
   constexpr bool kF32T = std::is_same_v<T, float>;
-  constexpr int KT = L::kKeys, U = KT / 32, ND = D / 32;
-  constexpr int kSteps = kF32T ? D / 8 : D / 16;  // of the score product: two pieces of a key's row each
-  using Frag = std::conditional_t<kF32T, float4v, std::conditional_t<std::is_same_v<T, bf16>, bf16x8, half8>>;
-  static_assert(L::kLoads % W == 0);
-  __shared__ uint4v lds[4 * L::kBytes / 16];  // K, V, K, V
+  constexpr int U = KT / 32 / S, DW = D / H, ND = DW / 32, kGroups = W / (S * H);
+  constexpr int kSteps = DW / 16;       // of the score product: two pieces of a key's row each
+  constexpr int P = kF32T ? 3 : 1;      // pieces of an element
+  using Frag = std::conditional_t<std::is_same_v<T, _Float16>, half8, bf16x8>;
+  static_assert(kF32T || L::kLoads % W == 0);
+  __shared__ uint4v lds[(L::kLds + (H > 1 ? W * 4096 : 0)) / 16];
   const PromptBatch& b = a.b;
   const int lane = threadIdx.x & 63, wave = wave_id(), col = lane % 32, h = lane / 32;
+  const int key0 = wave % S * 32, dim0 = wave % H * DW;  // this wavefront's keys of a tile, its dims
   const int kv = blockIdx.x % b.n_kv;
   int seq, tile;
-  if (!find_tile(a, kCols * W, blockIdx.x / b.n_kv, &seq, &tile)) return;
+  if (!find_tile(a, kCols * kGroups, blockIdx.x / b.n_kv, &seq, &tile)) return;
 
   // the sequence: query rows q0 .., keys k0 .. k0 + len - 1; row r stands at key r + at0
   int64_t q0 = b.cu_q[seq], q1 = b.cu_q[seq + 1], k0 = b.cu_k[seq], k1 = b.cu_k[seq + 1];
@@ -187,8 +217,8 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void attn_prompt_kernel(P
     return static_cast<int>(lo < 0 ? 0 : (lo < len ? lo : len));
   };
   auto row_of = [&](int64_t c) { return static_cast<int>((c < n_cols ? c : n_cols - 1) / a.group); };
-  const int64_t wg_col = static_cast<int64_t>(tile) * kCols * W, my_col = wg_col + wave * kCols;
-  const int wg_hi = hi_of(row_of(wg_col + kCols * W - 1)), wg_lo = lo_of(row_of(wg_col)) & -KT;
+  const int64_t wg_col = static_cast<int64_t>(tile) * kCols * kGroups, my_col = wg_col + wave / (S * H) * kCols;
+  const int wg_hi = hi_of(row_of(wg_col + kCols * kGroups - 1)), wg_lo = lo_of(row_of(wg_col)) & -KT;
   const int first = row_of(my_col), last = row_of(my_col + kCols - 1);
   const bool idle = my_col >= n_cols;
   const int hi_max = idle ? 0 : hi_of(last), hi_min = hi_of(first), lo_min = lo_of(first), lo_max = lo_of(last);
@@ -198,53 +228,92 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void attn_prompt_kernel(P
   // a negative scale turns q around, so that the largest product is the largest score
   const float c = fabsf(a.scale) * 1.4426950408889634f;
 
-  // loads of a tile: instruction j of this wavefront fills 1 KB from row (j W + wave) 1024 / kRow on
-  constexpr int kMine = L::kLoads / W;
+  // loads of a tile.  16 bit: instruction j of this wavefront fills 1 KB of LDS; f32: pieces of 8 elements to
+  // registers, to be split
+  constexpr int kMine = kF32T ? (KT * L::kPieces + 64 * W - 1) / (64 * W) : L::kLoads / W;
+  constexpr int kPieceBytes = 8 * sizeof(T);
   uint32_t k_at[kMine], v_at[kMine];
   const uint32_t ks = static_cast<uint32_t>(b.k_stride * sizeof(T)), vs = static_cast<uint32_t>(b.v_stride * sizeof(T));
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     const int piece = (j * W + wave) * 64 + lane, r = piece / L::kPieces, p = piece % L::kPieces;
-    k_at[j] = r * ks + (p ^ L::k_swizzle(r)) * 16;
-    v_at[j] = r * vs + (p ^ L::v_swizzle(r)) * 16;
+    k_at[j] = r * ks + (kF32T ? p : p ^ L::k_swizzle(r)) * kPieceBytes;
+    v_at[j] = r * vs + (kF32T ? p : p ^ L::v_swizzle(r)) * kPieceBytes;
   }
   const T* const k_base = static_cast<const T*>(a.k) + k0 * b.k_stride + kv * D;
   const T* const v_base = static_cast<const T*>(a.v) + k0 * b.v_stride + kv * D;
   uint8_t* const lds8 = reinterpret_cast<uint8_t*>(lds);
+  uint4v raw[2][kF32T ? kMine : 1][2];  // f32: K and V pieces on their way
   auto fetch = [&](int t, int buf) {
     const int n = len - t < KT ? len - t : KT;  // rows that are keys; the rest is zeros
-    auto kr = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(k_base + t * b.k_stride), 0, (n - 1) * ks + L::kRow, 0x00027000);
-    auto vr = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(v_base + t * b.v_stride), 0, (n - 1) * vs + L::kRow, 0x00027000);
-    uint8_t* to = lds8 + buf * 2 * L::kBytes;
+    const int row_bytes = D * sizeof(T);
+    auto kr = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(k_base + t * b.k_stride), 0, (n - 1) * ks + row_bytes, 0x00027000);
+    auto vr = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(v_base + t * b.v_stride), 0, (n - 1) * vs + row_bytes, 0x00027000);
+    if constexpr (kF32T) {
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) load_to_lds(kr, to + (j * W + wave) * 1024, k_at[j], 0);
+      for (int j = 0; j < kMine; ++j) {
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) load_to_lds(vr, to + L::kBytes + (j * W + wave) * 1024, v_at[j], 0);
+        for (int i = 0; i < 2; ++i) {
+          raw[0][j][i] = __builtin_amdgcn_raw_buffer_load_b128(kr, k_at[j] + 16 * i, 0, 0);
+          raw[1][j][i] = __builtin_amdgcn_raw_buffer_load_b128(vr, v_at[j] + 16 * i, 0, 0);
+        }
+      }
+    } else {
+      uint8_t* to = lds8 + buf * 2 * L::kBytes;
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) load_to_lds(kr, to + (j * W + wave) * 1024, k_at[j], 0);
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) load_to_lds(vr, to + L::kBytes + (j * W + wave) * 1024, v_at[j], 0);
+    }
+  };
+  // f32: the fetched pieces to the planes (K hi, mid, lo, V hi, mid, lo)
+  auto store_planes = [&]() {
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int piece = (j * W + wave) * 64 + lane, r = piece / L::kPieces, p = piece % L::kPieces;
+      if (KT * L::kPieces % (64 * W) != 0 && piece >= KT * L::kPieces) break;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(raw[v][j][i / 4][i % 4]);
+        bf16x8 piece3[3];
+        split8(x, &piece3[0], &piece3[1], &piece3[2]);
+        const int at = r * L::kRow + (p ^ (v ? L::v_swizzle(r) : L::k_swizzle(r))) * 16;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) *reinterpret_cast<bf16x8*>(lds8 + (3 * v + e) * L::kBytes + at) = piece3[e];
+      }
+    }
   };
   const int tiles = wg_hi > wg_lo ? (wg_hi - wg_lo + KT - 1) / KT : 0;
   if (tiles > 0) fetch(wg_lo, 0);
 
-  Frag qf[kSteps];
+  Frag qf[kSteps][P];
   {
-    const T* p = static_cast<const T*>(a.q) + (q0 + row) * b.q_stride + static_cast<int64_t>(head) * D + h * L::kPer;
+    const T* p = static_cast<const T*>(a.q) + (q0 + row) * b.q_stride + static_cast<int64_t>(head) * D + dim0 + h * 8;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      qf[s] = *reinterpret_cast<const Frag*>(p + s * 2 * L::kPer);
-      if (a.scale < 0.0f) qf[s] = -qf[s];
+      if constexpr (kF32T) {
+        float x[8];
+        load8(p + s * 16, x);
+        split8(x, &qf[s][0], &qf[s][1], &qf[s][2]);
+      } else {
+        qf[s][0] = *reinterpret_cast<const Frag*>(p + s * 16);
+      }
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        if (a.scale < 0.0f) qf[s][e] = -qf[s][e];
+      }
     }
   }
   // places in LDS: piece 2 s + h of K row col; the V pieces of dims 32 d ..
   int k_lds[kSteps], v_lds[ND];
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) k_lds[s] = col * L::kRow + ((2 * s + h) ^ L::k_swizzle(col)) * 16;
+  for (int s = 0; s < kSteps; ++s) k_lds[s] = col * L::kRow + ((dim0 / 8 + 2 * s + h) ^ L::k_swizzle(col)) * 16;
 #pragma unroll
   for (int d = 0; d < ND; ++d) {
-    if constexpr (kF32T) {
-      v_lds[d] = 4 * h * L::kRow + ((8 * d + col / 4) ^ L::v_swizzle(4 * h)) * 16 + col % 4 * 4;
-    } else {
-      const int i = lane % 16, r = 4 * h + i / 4, p = 4 * d + 2 * (lane / 16 % 2) + i % 4 / 2;
-      v_lds[d] = r * L::kRow + (p ^ L::v_swizzle(r)) * 16 + i % 2 * 8;
-    }
+    const int i = lane % 16, r = 4 * h + i / 4, p = dim0 / 8 + 4 * d + 2 * (lane / 16 % 2) + i % 4 / 2;
+    v_lds[d] = r * L::kRow + (p ^ L::v_swizzle(r)) * 16 + i % 2 * 8;
   }
 
   float m = -FLT_MAX, lim = -FLT_MAX, l = 0.0f;
@@ -256,32 +325,62 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void attn_prompt_kernel(P
   }
   for (int n = 0; n < tiles; ++n) {
     const int t = wg_lo + n * KT;
-    wait_loads<0>();
-    __syncthreads();
-    if (n + 1 < tiles) fetch(t + KT, (n + 1) & 1);
-    if (t >= hi_max || t + KT <= lo_min) continue;
-    const uint8_t* const kt = lds8 + (n & 1) * 2 * L::kBytes;
-    const uint8_t* const vt = kt + L::kBytes;
+    if constexpr (kF32T) {
+      __syncthreads();  // the planes have been read
+      store_planes();
+      if (n + 1 < tiles) fetch(t + KT, 0);
+      __syncthreads();
+    } else {
+      wait_loads<0>();
+      __syncthreads();
+      if (n + 1 < tiles) fetch(t + KT, (n + 1) & 1);
+    }
+    const int tw = t + key0;
+    const bool on = tw < hi_max && tw + 32 * U > lo_min;
+    if (H == 1 && !on) continue;
+    const uint8_t* const kt = lds8 + (kF32T ? 0 : (n & 1) * 2 * L::kBytes) + key0 * L::kRow;
+    const uint8_t* const vt = kt + P * L::kBytes;
     float16v s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (H > 1 && !on) break;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
-        const Frag kf = *reinterpret_cast<const Frag*>(kt + u * 32 * L::kRow + k_lds[j]);
-        if constexpr (kF32T) {
+        Frag kf[P];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[u] = __builtin_amdgcn_mfma_f32_32x32x2f32(kf[e], qf[j][e], s[u], 0, 0, 0);
+        for (int e = 0; e < P; ++e) kf[e] = *reinterpret_cast<const Frag*>(kt + e * L::kBytes + u * 32 * L::kRow + k_lds[j]);
+        if constexpr (kF32T) {
+          s[u] = product6(kf, qf[j], s[u]);
         } else if constexpr (std::is_same_v<T, bf16>) {
-          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], s[u], 0, 0, 0);
+          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[0], qf[j][0], s[u], 0, 0, 0);
         } else {
-          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[j], s[u], 0, 0, 0);
+          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[0], qf[j][0], s[u], 0, 0, 0);
         }
       }
     }
-    if (t + KT > hi_min || t < lo_max) {
-      const int lo = lo_q - t - 4 * h, hi = hi_q - t - 4 * h;
+    if constexpr (H > 1) {  // every wavefront of the workgroup comes by here
+      float4v* const part = reinterpret_cast<float4v*>(lds8 + L::kLds);
+      if (on) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          part[(wave * 4 + i) * 64 + lane] = float4v{s[0][4 * i], s[0][4 * i + 1], s[0][4 * i + 2], s[0][4 * i + 3]};
+      }
+      __syncthreads();
+      if (!on) continue;
+#pragma unroll
+      for (int w = 1; w < H; ++w) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4v x = part[((wave / H * H + (wave + w) % H) * 4 + i) * 64 + lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[0][4 * i + e] += x[e];
+        }
+      }
+    }
+    if (tw + 32 * U > hi_min || tw < lo_max) {
+      const int lo = lo_q - tw - 4 * h, hi = hi_q - tw - 4 * h;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -314,66 +413,114 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void attn_prompt_kernel(P
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if constexpr (kF32T) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+      for (int g = 0; g < 2; ++g) {
+        Frag pf[P];
+        if constexpr (kF32T) {
+          float x[8];
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const float vf = *reinterpret_cast<const float*>(vt + (32 * u + 8 * (i / 4) + i % 4) * L::kRow + v_lds[d]);
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, s[u][i], o[d], 0, 0, 0);
-          }
+          for (int i = 0; i < 8; ++i) x[i] = s[u][8 * g + i];
+          split8(x, &pf[0], &pf[1], &pf[2]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pf[0][i] = static_cast<T>(s[u][8 * g + i]);
         }
-      } else {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          Frag pf;
+        for (int d = 0; d < ND; ++d) {
+          Frag vf[P];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) pf[i] = static_cast<T>(s[u][8 * g + i]);
-#pragma unroll
-          for (int d = 0; d < ND; ++d) {
+          for (int e = 0; e < P; ++e) {
             typedef __attribute__((address_space(3))) short4v lds_short4;
-            const uint8_t* p = vt + (32 * u + 16 * g) * L::kRow + v_lds[d];
+            const uint8_t* p = vt + e * L::kBytes + (32 * u + 16 * g) * L::kRow + v_lds[d];
             const short4v v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)p);
             const short4v v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(p + 8 * L::kRow));
-            const Frag vf = __builtin_bit_cast(Frag, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-            if constexpr (std::is_same_v<T, bf16>) {
-              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
-            } else {
-              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf, o[d], 0, 0, 0);
-            }
+            vf[e] = __builtin_bit_cast(Frag, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+          }
+          if constexpr (kF32T) {
+            o[d] = product6(vf, pf, o[d]);
+          } else if constexpr (std::is_same_v<T, bf16>) {
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[0], pf[0], o[d], 0, 0, 0);
+          } else {
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[0], pf[0], o[d], 0, 0, 0);
           }
         }
       }
     }
   }
-  if (idle) return;
-
   const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
   l = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+  if constexpr (S > 1) {
+    // the group's states into one, through the tiles' LDS: of the output each wavefront then has every S-th tile
+    static_assert(S * (ND * 16 + 2) * 256 <= L::kLds && kGroups == 1);
+    float* const ml = reinterpret_cast<float*>(lds8);
+    float4v* const os = reinterpret_cast<float4v*>(lds8 + S * 512);
+    __syncthreads();
+    ml[(2 * wave) * 64 + lane] = m, ml[(2 * wave + 1) * 64 + lane] = l;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        os[((wave * ND + d) * 4 + i) * 64 + lane] = float4v{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+    }
+    __syncthreads();
+    float f[S];
+    m = -FLT_MAX, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < S; ++w) m = fmaxf(m, ml[2 * w * 64 + lane]);
+#pragma unroll
+    for (int w = 0; w < S; ++w) {
+      f[w] = __builtin_amdgcn_exp2f(ml[2 * w * 64 + lane] - m);
+      l += f[w] * ml[(2 * w + 1) * 64 + lane];
+    }
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      if (d % S != wave) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float4v v = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < S; ++w) v += os[((w * ND + d) * 4 + i) * 64 + lane] * f[w];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][4 * i + e] = v[e];
+      }
+    }
+  }
+  if (idle) return;
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   bool finite = true;
 #pragma unroll
   for (int d = 0; d < ND; ++d) {
+    if (S > 1 && d % S != wave) continue;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       o[d][i] *= inv;
       finite = finite && fabsf(o[d][i]) <= FLT_MAX;
     }
   }
-  if (__any(!finite)) {
-    for (int i = 0; i < kCols && my_col + i < n_cols; ++i) {
+  bool again = __any(!finite);
+  if constexpr (S > 1) {  // by every wavefront of the group, if one of them has to
+    int* const flags = reinterpret_cast<int*>(lds8 + S * 512 + S * ND * 4096);
+    static_assert(S * 512 + S * ND * 4096 + S * 4 <= L::kLds);
+    if (lane == 0) flags[wave] = again;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < S; ++w) again = again || flags[w] != 0;
+  }
+  if (again) {
+    for (int i = wave % S; i < kCols && my_col + i < n_cols; i += S) {
       const int r = row_of(my_col + i);
       const int64_t hd = static_cast<int64_t>(kv) * a.group + (my_col + i - static_cast<int64_t>(r) * a.group);
       column_by_keys<T, D>(static_cast<const T*>(a.q) + (q0 + r) * b.q_stride + hd * D, k_base, v_base, b.k_stride, b.v_stride,
-                           lo_of(r), hi_of(r), a.scale * 1.4426950408889634f,
+                           lo_of(r), hi_of(r), a.scale * 1.4426950408889634f, dim0, DW,
                            static_cast<T*>(a.out) + ((q0 + r) * b.n_heads + hd) * D);
     }
     return;
   }
   if (c_at >= n_cols) return;
-  T* out = static_cast<T*>(a.out) + ((q0 + row) * b.n_heads + head) * D + 4 * h;
+  T* out = static_cast<T*>(a.out) + ((q0 + row) * b.n_heads + head) * D + dim0 + 4 * h;
 #pragma unroll
   for (int d = 0; d < ND; ++d) {
+    if (S > 1 && d % S != wave) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       typedef T t4 __attribute__((ext_vector_type(4)));
@@ -385,22 +532,30 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void attn_prompt_kernel(P
   }
 }
 
-template <typename T, int D, int W>
+template <typename T, int D, int W, int KT, int S, int H>
 hipError_t run(const PromptArgs& a, hipStream_t s) {
   // every column, and a part-filled tile to a sequence
   const int64_t seqs = a.b.n_seq < a.b.n_q ? a.b.n_seq : a.b.n_q;
-  const int64_t tiles = a.b.n_q * a.group / (kCols * W) + seqs;
+  const int64_t tiles = a.b.n_q * a.group / (kCols * W / (S * H)) + seqs;
   unsigned gx = 0;
   if (tiles > INT32_MAX / 64 || !launch_grid(tiles * a.b.n_kv, 64 * W, &gx)) return hipErrorInvalidConfiguration;
-  attn_prompt_kernel<T, D, W><<<gx, 64 * W, 0, s>>>(a);
+  attn_prompt_kernel<T, D, W, KT, S, H><<<gx, 64 * W, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, int D>
 hipError_t prompt_w(const PromptArgs& a, hipStream_t s) {
-  // Wavefronts of a workgroup.  4 and 8 are alike where there is work for all (550 and 560 us for 8192 rows of 32 / 8
-  // heads of 128 f16), f32 has less LDS left and is better with 4 (160, 192 us); few rows fill more CUs with 2.
-  return a.b.n_q * a.b.n_heads >= 256 * kCols * 4 ? run<T, D, 4>(a, s) : run<T, D, 2>(a, s);
+  const bool few = a.b.n_q * a.b.n_heads < kFewGroups * kCols;
+  if constexpr (std::is_same_v<T, float> && D == 256) {
+    // the pieces of 256 dims do not fit a wavefront's registers
+    return few ? run<T, D, 2, 32, 1, 2>(a, s) : run<T, D, 8, 32, 1, 2>(a, s);
+  } else {
+    constexpr bool kF32 = std::is_same_v<T, float>;
+    constexpr int kWide = kF32 && D > 64 ? 32 : 64;
+    // keys of a tile that is shared out over wavefronts: as many as LDS holds
+    constexpr int kNarrow = kF32 ? (D <= 96 ? 128 : 64) : (D <= 128 ? 128 : 64);
+    return few ? run<T, D, kNarrow / 32, kNarrow, kNarrow / 32, 1>(a, s) : run<T, D, 4, kWide, 1, 1>(a, s);
+  }
 }
 
 template <typename T>
