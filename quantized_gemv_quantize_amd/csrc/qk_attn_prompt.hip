@@ -546,14 +546,15 @@ hipError_t run(const PromptArgs& a, hipStream_t s) {
 template <typename T, int D>
 hipError_t prompt_w(const PromptArgs& a, hipStream_t s) {
   const bool few = a.b.n_q * a.b.n_heads < kFewGroups * kCols;
-  if constexpr (std::is_same_v<T, float> && D == 256) {
-    // the pieces of 256 dims do not fit a wavefront's registers
-    return few ? run<T, D, 2, 32, 1, 2>(a, s) : run<T, D, 8, 32, 1, 2>(a, s);
+  if constexpr (std::is_same_v<T, float> && D >= 128) {
+    // The pieces of so many dims want more registers than a wavefront has: dims are shared out too.  1500 rows of
+    // 3 heads, 1500 of 20 (D = 256): by 8 wavefronts and by 2 159 and 284 us, by none 412 and 414.
+    return few ? run<T, D, D / 32, 32, 1, D / 32>(a, s) : run<T, D, 8, 32, 1, 2>(a, s);
   } else {
     constexpr bool kF32 = std::is_same_v<T, float>;
     constexpr int kWide = kF32 && D > 64 ? 32 : 64;
     // keys of a tile that is shared out over wavefronts: as many as LDS holds
-    constexpr int kNarrow = kF32 ? (D <= 96 ? 128 : 64) : (D <= 128 ? 128 : 64);
+    constexpr int kNarrow = D <= 128 ? 128 : 64;
     return few ? run<T, D, kNarrow / 32, kNarrow, kNarrow / 32, 1>(a, s) : run<T, D, 4, kWide, 1, 1>(a, s);
   }
 }
