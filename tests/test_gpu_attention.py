@@ -367,6 +367,46 @@ def test_paged_garbage_in_masked_places(torch_cuda, dtype):
         _check(dtype, got, *_paged_want(c, fq, new, start, np.float64(np.float32(dim ** -0.5)), window), 72, dim)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n_seq", [65, 150])
+def test_paged_many_sequences_shared_out(torch_cuda, dtype, n_seq):
+    """More sequences than a wavefront has lanes, empty ones among them, long enough to be cut into ranges:
+    items that one range holds, that two share, and that many do."""
+    rng = np.random.default_rng(n_seq)
+    new = [int(x) for x in rng.integers(0, 3, n_seq)]
+    start = [int(x) for x in rng.integers(0, 400, n_seq)]
+    start[n_seq // 2], start[-1] = 5000, 1500
+    _paged_case(torch_cuda, 15, dtype, 64, 2, 6, 32, new, start)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("window", [0, 40, 900])
+def test_paged_ranges_with_windows(torch_cuda, dtype, window):
+    _paged_case(torch_cuda, 16, dtype, 128, 2, 16, 64, [4, 1, 9], [2500, 1024, 3000], window=window)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_paged_small_zero_and_growing_value_scales(torch_cuda, dtype):
+    """Value scales that are tiny throughout, 0 in some blocks, and that grow along the cache (the power of two
+    that weights are kept by has to follow)."""
+    torch = torch_cuda
+    dim, page, n = 64, 16, 700
+    half = page * (dim // 2 + dim // 16)
+    for k, exps in enumerate((np.full(n, -18.0), np.linspace(-20, 14, n), np.linspace(14, -20, n))):
+        rng = np.random.default_rng(80 + k)
+        c = Cache(torch, rng, [n], 2, dim, page)
+        for t in range(n):
+            sc = (2.0 ** exps[t] * rng.uniform(0.5, 1.0, (2, dim // 32))).astype(np.float16)
+            if t % 7 == 3:
+                sc[:, 0] = 0
+            a = half + page * dim // 2 + t % page * dim // 16
+            c.raw[c.table[0, t // page], :, a:a + dim // 16] = sc.view(np.uint8).reshape(2, -1)
+        c.pages.copy_(torch.from_numpy(c.raw))
+        tq, fq = typed(torch, rng.standard_normal((2, 4, dim)), dtype)
+        got = qk.qk_attn_paged(c.pages, page, c.dtable, i32(torch, [0, 2]), i32(torch, [n - 2]), tq)
+        _check(dtype, got, *_paged_want(c, fq, [2], [n - 2], np.float64(np.float32(dim ** -0.5)), 0), n, dim)
+
+
 def test_paged_offsets_past_32_bits(torch_cuda):
     """A cache of more than 4 GiB whose last pages are in use."""
     torch = torch_cuda
@@ -540,6 +580,44 @@ def test_prompt_chunks_and_empty_rows(torch_cuda, dtype, dim, causal):
 @pytest.mark.parametrize("dtype", TYPES)
 def test_prompt_long(torch_cuda, dtype):
     _prompt_case(torch_cuda, 25, dtype, 64, 1, 1, [1500, 700])
+
+
+# Enough columns (rows x heads) for a wavefront to each 32 of them; the tests above stay below.
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+def test_prompt_wide(torch_cuda, dtype, dim):
+    _prompt_case(torch_cuda, 32, dtype, dim, 2, 32, [260, 1, 0, 129, 64, 65], strided=dim == 128)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("causal,window", [(True, 50), (False, 0), (False, 100)])
+def test_prompt_wide_masks_and_chunks(torch_cuda, dtype, dim, causal, window):
+    """More keys than rows, fewer (rows that see nothing), none."""
+    _prompt_case(torch_cuda, 33, dtype, dim, 4, 20, [400, 300, 9, 130], [470, 237, 0, 331], causal=causal, window=window)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("heads", [2, 64])
+def test_prompt_nan_stays_where_it_is_seen(torch_cuda, dtype, dim, heads):
+    """Few columns and many: keys that are NaN and values that are infinite touch the rows that see
+    them and no others."""
+    torch = torch_cuda
+    rng = np.random.default_rng(34)
+    cu, seen = [0, 170, 260], 150
+    (tq, fq), (tk, fk), (tv, fv) = (typed(torch, rng.standard_normal((260, h, dim)), dtype) for h in (heads, 2, 2))
+    want = _prompt_want(fq, fk, fv, cu, cu, np.float64(np.float32(dim ** -0.5)), True, 0)
+    tv[seen, 0] = float("inf")
+    tk[seen + 5, 1] = float("nan")
+    got = qk.qk_attn_prompt(tq, tk, tv, i32(torch, cu))
+    clean = np.r_[0:seen, 170:260]
+    _check(dtype, got[clean], *(a[clean] for a in want), 170, dim)
+    g = heads // 2
+    assert (got[seen:170, :g] == float("inf")).all()
+    assert torch.isnan(got[seen + 5:170, g:].float()).all()
+    _check(dtype, got[seen:seen + 5, g:], *(a[seen:seen + 5, g:] for a in want), 170, dim)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
