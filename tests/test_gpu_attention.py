@@ -700,3 +700,16 @@ def test_chunked_prompt_through_the_cache(torch_cuda):
     want = _paged_want(c, qr.double().cpu().numpy(), [80], [150], np.float64(np.float32(dim ** -0.5)), 0)
     _check("f32", one, *want, 230, dim)
     _check("f32", two, *want, 230, dim)
+
+
+def test_example_layer(torch_cuda):
+    """examples/attention_layer.py: chunks and decode steps through the cache.  Both attentions are within the f32
+    bound of the same sums (2^-17 here), but the output projection quantizes them to 8 bits (Q8_K): a value at
+    the border of two codes may move by one of 127 steps of its block's largest."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_layer.py")
+    spec = importlib.util.spec_from_file_location("attention_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main(hidden=512, heads=4, kv_heads=2, dim=128, lengths=(150, 40), chunk=64, steps=5) < 1 / 127
