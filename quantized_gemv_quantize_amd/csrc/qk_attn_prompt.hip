@@ -216,7 +216,10 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void attn_prompt_kernel(P
     const int64_t lo = b.window > 0 ? r + at0 - b.window + 1 : 0;
     return static_cast<int>(lo < 0 ? 0 : (lo < len ? lo : len));
   };
-  auto row_of = [&](int64_t c) { return static_cast<int>((c < n_cols ? c : n_cols - 1) / a.group); };
+  // columns fit 31 bits (2^21 rows of 2^10 heads at most), which a division in 64 would not make use of
+  auto row_of = [&](int64_t c) {
+    return static_cast<int>(static_cast<uint32_t>(c < n_cols ? c : n_cols - 1) / static_cast<uint32_t>(a.group));
+  };
   const int64_t wg_col = static_cast<int64_t>(tile) * kCols * kGroups, my_col = wg_col + wave / (S * H) * kCols;
   const int wg_hi = hi_of(row_of(wg_col + kCols * kGroups - 1)), wg_lo = lo_of(row_of(wg_col)) & -KT;
   const int first = row_of(my_col), last = row_of(my_col + kCols - 1);
