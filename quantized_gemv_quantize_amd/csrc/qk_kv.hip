@@ -1,6 +1,7 @@
 // qk_kv.hip - writing rows to the paged Q4_0 cache (position rotation and quantization
 // on the way) and reading them back.
 #include <climits>
+#include <type_traits>
 
 #include "qk_internal.h"
 #include "qk_kv.h"
@@ -84,8 +85,10 @@ struct Shape {
 };
 // Heads of a thread.  Append: each turned by the same angles, read once; 2, 4, 8 measured 130, 122 and 106 us (with
 // the read back, 7380 rows of 32 + 2 x 32 heads of 128 f16).  Read: 2, 4, 8 measured 34.4, 28.8, 29.9 us (28 K rows of
-// 2 x 8 heads of 128 bf16, 6.0 TB/s).
+// 2 x 8 heads of 128 bf16, 6.0 TB/s).  Where that leaves most of the card without work, one head of a thread
+// ends sooner (append of 64 rows of 32 + 2 x 8 heads: 4.4 us against 8.2).
 constexpr int kAppendJobs = 8, kReadJobs = 4;
+constexpr int64_t kManyGroups = 512;  // workgroups
 
 struct Place {
   int64_t row, pos, page;  // page -1: none
@@ -123,7 +126,7 @@ __device__ __forceinline__ Place place_of(const KvBatch& b) {
 
 // Memory bound: k, v and q are read once from HBM (a rotated half's partner comes from the same lines), 9/16
 // byte per key and value dim is written.
-template <typename T, int D, bool kHalves>
+template <typename T, int D, bool kHalves, int kJobs>
 __global__ __launch_bounds__(Shape<D>::kThreads) void kv_append_kernel(KvBatch b, uint8_t* pages, const T* k, int64_t k_stride,
                                                                        const T* v, int64_t v_stride, const T* q, int64_t q_stride,
                                                                        int n_heads, const float* rope, int64_t rope_rows, int n_rot,
@@ -133,7 +136,7 @@ __global__ __launch_bounds__(Shape<D>::kThreads) void kv_append_kernel(KvBatch b
   if (!at.listed || (n_rot > 0 && (at.pos < 0 || at.pos >= rope_rows))) return;
   const int e0 = threadIdx.x % Shape<D>::kPieces * 8;
   // heads in the order K, V, q
-  const int head0 = blockIdx.y * kAppendJobs, heads = 2 * b.n_kv + n_heads;
+  const int head0 = blockIdx.y * kJobs, heads = 2 * b.n_kv + n_heads;
   const bool turns = e0 < n_rot, low = e0 < n_rot / 2;
   const int partner = kHalves && turns ? (low ? n_rot / 2 : -(n_rot / 2)) : 0;
   float4v cs[4] = {};
@@ -145,9 +148,9 @@ __global__ __launch_bounds__(Shape<D>::kThreads) void kv_append_kernel(KvBatch b
       if (kHalves && low) cs[i][1] = -cs[i][1], cs[i][3] = -cs[i][3];
     }
   }
-  float x[kAppendJobs][8], o[kAppendJobs][8];
+  float x[kJobs][8], o[kJobs][8];
 #pragma unroll
-  for (int j = 0; j < kAppendJobs; ++j) {
+  for (int j = 0; j < kJobs; ++j) {
     const int h = head0 + j;
     if (h >= heads) break;
     const T* p = h < b.n_kv ? k + at.row * k_stride + h * D
@@ -158,7 +161,7 @@ __global__ __launch_bounds__(Shape<D>::kThreads) void kv_append_kernel(KvBatch b
   }
   const int64_t tokens = int64_t(1) << b.page_shift, slot = at.pos & (tokens - 1), half = kv_half_bytes(tokens, D);
 #pragma unroll
-  for (int j = 0; j < kAppendJobs; ++j) {
+  for (int j = 0; j < kJobs; ++j) {
     const int h = head0 + j;
     if (h >= heads) break;
     const bool is_v = h >= b.n_kv && h < 2 * b.n_kv;
@@ -178,16 +181,16 @@ __global__ __launch_bounds__(Shape<D>::kThreads) void kv_append_kernel(KvBatch b
 }
 
 // Code dwords of the rows' K, then V heads; value = d * (code - 8), exact in f32, rounded once to T.
-template <typename T, int D>
+template <typename T, int D, int kJobs>
 __global__ __launch_bounds__(Shape<D>::kThreads) void kv_read_kernel(KvBatch b, const uint8_t* pages, T* k_out, T* v_out) {
   constexpr int NB = D / 32;
   const Place at = place_of<D>(b);
   if (!at.listed) return;
-  const int e = threadIdx.x % Shape<D>::kPieces, head0 = blockIdx.y * kReadJobs;
+  const int e = threadIdx.x % Shape<D>::kPieces, head0 = blockIdx.y * kJobs;
   const int64_t tokens = int64_t(1) << b.page_shift, slot = at.pos & (tokens - 1), half = kv_half_bytes(tokens, D);
-  uint32_t code[kReadJobs] = {}, scale[kReadJobs] = {};
+  uint32_t code[kJobs] = {}, scale[kJobs] = {};
 #pragma unroll
-  for (int j = 0; j < kReadJobs; ++j) {
+  for (int j = 0; j < kJobs; ++j) {
     const int h = head0 + j, is_v = h >= b.n_kv;
     if (h >= 2 * b.n_kv || at.page < 0) break;
     const uint8_t* base = pages + (at.page * b.n_kv + h - is_v * b.n_kv) * 2 * half + is_v * half;
@@ -195,7 +198,7 @@ __global__ __launch_bounds__(Shape<D>::kThreads) void kv_read_kernel(KvBatch b, 
     scale[j] = *reinterpret_cast<const uint16_t*>(base + tokens * (D / 2) + (slot * NB + e % NB) * 2);
   }
 #pragma unroll
-  for (int j = 0; j < kReadJobs; ++j) {
+  for (int j = 0; j < kJobs; ++j) {
     const int h = head0 + j, is_v = h >= b.n_kv;
     if (h >= 2 * b.n_kv) break;
     const half8 c = nibbles_to_f16(code[j]);
@@ -217,14 +220,31 @@ hipError_t launch(Kernel kernel, const KvBatch& b, int64_t heads, hipStream_t s,
   kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), S::kThreads, 0, s>>>(b, args...);
   return hipGetLastError();
 }
+template <int D>
+bool many_groups(const KvBatch& b, int64_t heads, int jobs) {
+  return (b.n_rows + Shape<D>::kRows - 1) / Shape<D>::kRows * ((heads + jobs - 1) / jobs) >= kManyGroups;
+}
 
 template <typename T, int D>
 hipError_t append_d(const KvBatch& b, uint8_t* pages, const void* k, int64_t ks, const void* v, int64_t vs, const void* q,
                     int64_t qs, int n_heads, const float* rope, int64_t rope_rows, int n_rot, int halves, void* q_out,
                     hipStream_t s) {
-  return launch<D, kAppendJobs>(halves ? kv_append_kernel<T, D, true> : kv_append_kernel<T, D, false>, b, 2 * int64_t(b.n_kv) + n_heads, s, pages,
-                   static_cast<const T*>(k), ks, static_cast<const T*>(v), vs, static_cast<const T*>(q), qs, n_heads, rope, rope_rows,
-                   n_rot, static_cast<T*>(q_out));
+  const int64_t heads = 2 * int64_t(b.n_kv) + n_heads;
+  auto run = [&](auto jobs) {
+    constexpr int kJobs = decltype(jobs)::value;
+    return launch<D, kJobs>(halves ? kv_append_kernel<T, D, true, kJobs> : kv_append_kernel<T, D, false, kJobs>, b, heads, s, pages,
+                            static_cast<const T*>(k), ks, static_cast<const T*>(v), vs, static_cast<const T*>(q), qs, n_heads,
+                            rope, rope_rows, n_rot, static_cast<T*>(q_out));
+  };
+  return many_groups<D>(b, heads, kAppendJobs) ? run(std::integral_constant<int, kAppendJobs>{})
+                                               : run(std::integral_constant<int, 1>{});
+}
+
+template <typename T, int D>
+hipError_t read_d(const KvBatch& b, const uint8_t* pages, T* ko, T* vo, hipStream_t s) {
+  const int64_t heads = 2 * int64_t(b.n_kv);
+  return many_groups<D>(b, heads, kReadJobs) ? launch<D, kReadJobs>(kv_read_kernel<T, D, kReadJobs>, b, heads, s, pages, ko, vo)
+                                             : launch<D, 1>(kv_read_kernel<T, D, 1>, b, heads, s, pages, ko, vo);
 }
 
 template <typename T>
@@ -246,10 +266,10 @@ template <typename T>
 hipError_t read_t(const KvBatch& b, int dim, const uint8_t* pages, void* k_out, void* v_out, hipStream_t s) {
   T *ko = static_cast<T*>(k_out), *vo = static_cast<T*>(v_out);
   switch (dim) {
-    case 64: return launch<64, kReadJobs>(kv_read_kernel<T, 64>, b, 2 * int64_t(b.n_kv), s, pages, ko, vo);
-    case 96: return launch<96, kReadJobs>(kv_read_kernel<T, 96>, b, 2 * int64_t(b.n_kv), s, pages, ko, vo);
-    case 128: return launch<128, kReadJobs>(kv_read_kernel<T, 128>, b, 2 * int64_t(b.n_kv), s, pages, ko, vo);
-    default: return launch<256, kReadJobs>(kv_read_kernel<T, 256>, b, 2 * int64_t(b.n_kv), s, pages, ko, vo);
+    case 64: return read_d<T, 64>(b, pages, ko, vo, s);
+    case 96: return read_d<T, 96>(b, pages, ko, vo, s);
+    case 128: return read_d<T, 128>(b, pages, ko, vo, s);
+    default: return read_d<T, 256>(b, pages, ko, vo, s);
   }
 }
 

@@ -134,6 +134,30 @@ def test_append_and_read_bit_exact(torch_cuda, dtype, dim):
         _append_case(torch_cuda, rng, dtype, dim, hk, h, page, new, start, style, n_rot, strided=hk == 2)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("style", [qk.QK_ROPE_HALVES, qk.QK_ROPE_PAIRS])
+def test_append_and_read_many_rows(torch_cuda, dtype, dim, style):
+    """Rows enough for several heads to a thread: the same bytes as the same rows a few at a time."""
+    torch = torch_cuda
+    rng = np.random.default_rng(6)
+    hk, h, page, n = 9, 18, 32, 5000
+    c = Cache(torch, rng, [n], hk, dim, page)
+    q, k, v = (torch.randn(n, x, dim, device="cuda").to(dt(torch, dtype)) for x in (h, hk, hk))
+    rope = torch.from_numpy(ref.rope_table(n, dim // 2)).cuda()
+    one, few = c.pages.clone(), c.pages.clone()
+    q_one = qk.qk_kv_append(one, page, c.dtable, i32(torch, [0, n]), i32(torch, [0]), k, v, q=q, rope=rope, rope_style=style)
+    q_few, rows = [], []
+    for a in range(0, n, 250):
+        at = (few, page, c.dtable, i32(torch, [0, 250]), i32(torch, [a]))
+        q_few.append(qk.qk_kv_append(*at, k[a:a + 250], v[a:a + 250], q=q[a:a + 250], rope=rope, rope_style=style))
+        rows.append(qk.qk_kv_read(*at, 250, dim, dtype=dt(torch, dtype)))
+    assert torch.equal(one, few) and torch.equal(q_one, torch.cat(q_few))
+    got = qk.qk_kv_read(one, page, c.dtable, i32(torch, [0, n]), i32(torch, [0]), n, dim, dtype=dt(torch, dtype))
+    for i in range(2):
+        assert torch.equal(got[i], torch.cat([r[i] for r in rows]))
+
+
 def test_append_many_sequences(torch_cuda):
     """More sequences than a wavefront has lanes; empty ones among them."""
     rng = np.random.default_rng(5)
