@@ -330,7 +330,8 @@ int64_t qk_kv_page_bytes(int type, int64_t page_tokens, int64_t head_dim);
  *   pages      the cache, written.
  *   dtype      QK_TYPE_F32, QK_TYPE_F16 or QK_TYPE_BF16 (else QK_E_TYPE): k, v, q, q_out.
  *   k, v       rows of n_kv_heads * head_dim elements, k_stride / v_stride elements
- *              apart (a slice of a fused projection's output will do).
+ *              apart (a slice of a fused projection's output will do); strides of float
+ *              tensors are at most 2^23 elements, in every call (else QK_E_SHAPE).
  *   q          rows of n_heads * head_dim elements q_stride apart, or NULL: no queries.
  *   n_heads    query heads, 1 .. 1024 (with q NULL: ignored).
  *   rope       f32 [rope_rows][n_rot / 2][2]: cos and sin of each pair's angle at each

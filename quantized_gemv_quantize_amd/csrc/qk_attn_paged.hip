@@ -27,6 +27,11 @@
 // 0.  Such a tile (and one with a scale of 0, or a mask over an infinite or NaN scale) is taken in bf16 or f32: turning the codes into bf16
 // costs 96 of some 400 vector instructions a tile, f32 products 8 times the matrix time.
 //
+// Bound by memory and, close behind, by the vector instructions that take the codes apart (about 320 a
+// wavefront for 32 positions of 128 dims, 9 KB / us of cache for each SIMD).  Measured: 64 sequences of 61 .. 8190 on
+// 32 / 8 heads of 128 bf16, 314 MB: 78 us, 4.0 TB/s (a copy of 1 GiB reaches 5.0), of which the first
+// product starts after 5 us and the join takes 5; one sequence of 65502 (75 MB, f16): 28 us; of 317: 11 us.
+//
 // Work is split over the positions when the table allows more than kDirectSteps steps: all
 // items' steps laid end to end are cut into equal ranges, one a workgroup, however uneven
 // the sequences; ranges that hold a part of an item write (ref, sum, output) to the workspace and a
@@ -41,9 +46,12 @@ namespace qk {
 namespace {
 
 constexpr int kWaves = 4, kTile = 32, kStep = kWaves * kTile, kCols = 16;
-constexpr int kDirectSteps = 8;  // 1024 positions
+// 1024 positions: one sequence of 500, 900, 1500 takes 13, 18, 23 us whole and 17 each cut
+constexpr int kDirectSteps = 8;
 constexpr int kFixedUnits = 3;   // an item's start and end cost about as much as 3 of its steps (1 .. 4: 104, 98, 95, 94 us for 64 sequences of 61 .. 8190)
-constexpr int kMinUnits = 3;     // least units of a range
+// least units of a range: 3, 6, 8, 12 measured 23, 26, 26, 31 us (16 sequences of 2 .. 6 rows, window 2048) and
+// 31, 31, 34, 36 (one sequence of 65502)
+constexpr int kMinUnits = 3;
 
 // Workgroups that fit a CU by the registers of a lane (512 to a lane of the SIMD's wavefronts).
 constexpr int groups_per_cu(int dim, bool f32) { return dim > 128 ? 1 : (dim <= 64 ? 4 : 3) - (f32 && dim != 96 ? 1 : 0); }

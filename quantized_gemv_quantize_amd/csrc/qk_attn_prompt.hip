@@ -21,6 +21,11 @@
 // matrix time of mfma_32x32x2_f32.  Keys and values come through registers, are split once for the
 // workgroup and stored as three planes.
 //
+// Bound by the matrix units: a tile of 64 keys is 32 matrix instructions of 32 cycles and 176 vector ones (32 of
+// them exponentials at a quarter of the rate), about 1000 cycles each, of two wavefronts to a SIMD.  Measured:
+// 8192 rows, 32 / 8 heads of 128 f16, causal: 549 us, 1.00 PFLOP/s (a library product of 8192 cubed 1.08);
+// 7 prompts of 37 .. 2047 bf16: 136 us, 0.74, with 4 to 7 us of a workgroup's 27 before and after its tiles.
+//
 // A masked key's weight is 0, but 0 times an infinite or NaN value is NaN: a wavefront whose output is
 // not finite at the end computes its rows again key by key, over the visible keys only.
 #include <cfloat>

@@ -125,7 +125,7 @@ __device__ __forceinline__ Place place_of(const KvBatch& b) {
 }
 
 // Memory bound: k, v and q are read once from HBM (a rotated half's partner comes from the same lines), 9/16
-// byte per key and value dim is written.
+// byte per key and value dim is written.  Measured: 7380 rows of 32 + 2 x 32 heads of 128 f16, 272 MB: 67 us, 4.1 TB/s.
 template <typename T, int D, bool kHalves, int kJobs>
 __global__ __launch_bounds__(Shape<D>::kThreads) void kv_append_kernel(KvBatch b, uint8_t* pages, const T* k, int64_t k_stride,
                                                                        const T* v, int64_t v_stride, const T* q, int64_t q_stride,
