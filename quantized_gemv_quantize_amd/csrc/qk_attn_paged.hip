@@ -711,8 +711,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(PagedArgs a) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k * kWaves;
-      const float* p = part(i < task.parts ? i : i0);
-      r[k] = i < task.parts ? p[lane] : -FLT_MAX;
+      r[k] = -FLT_MAX, s[k] = 0.0f, x[k][0] = x[k][1] = float4v{0, 0, 0, 0};
+      if (i >= task.parts) continue;
+      const float* p = part(i);
+      r[k] = p[lane];
       s[k] = p[64 + lane];
 #pragma unroll
       for (int e = 0; e < 2; ++e) x[k][e] = reinterpret_cast<const float4v*>(p + 128)[(2 * y + e) * 64 + lane];
