@@ -23,8 +23,8 @@
 //
 // Bound by the matrix units: a tile of 64 keys is 32 matrix instructions of 32 cycles and 176 vector ones (32 of
 // them exponentials at a quarter of the rate), about 1000 cycles each, of two wavefronts to a SIMD.  Measured:
-// 8192 rows, 32 / 8 heads of 128 f16, causal: 549 us, 1.00 PFLOP/s (a library product of 8192 cubed 1.08);
-// 7 prompts of 37 .. 2047 bf16: 136 us, 0.74, with 4 to 7 us of a workgroup's 27 before and after its tiles.
+// 8192 rows, 32 / 8 heads of 128 f16, causal: 549 - 561 us, 0.98 - 1.00 PFLOP/s (a library product of 8192 cubed
+// 1.08); 7 prompts of 37 .. 2047 bf16: 127 us, 0.80, where a workgroup's start and end (4 to 7 us) show.
 //
 // A masked key's weight is 0, but 0 times an infinite or NaN value is NaN: a wavefront whose output is
 // not finite at the end computes its rows again key by key, over the visible keys only.
@@ -43,7 +43,7 @@ typedef short short4v __attribute__((ext_vector_type(4)));
 constexpr int kCols = 32;
 // Groups of 32 columns below which a group is shared by several wavefronts: with 140 groups of 1500 rows, 300 of 1200
 // and 600 of 600 (D = 128 bf16), 21, 21 and 30 us against 34, 30 and 20 with a wavefront to a group.
-constexpr int64_t kFewGroups = 512;
+constexpr int64_t kFewGroups = 512, kManyGroups = 4096;
 
 struct PromptArgs {
   PromptBatch b;
@@ -186,7 +186,7 @@ __device__ __forceinline__ void column_by_keys(const T* q, const T* k, const T* 
 // W wavefronts: W / (S H) groups of 32 columns.  A group is shared by S wavefronts that take 32 keys of a tile of KT each
 // (S = 1: all), or by H that take D / H dims each and add their scores up through LDS.
 template <typename T, int D, int W, int KT, int S, int H>
-__global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void attn_prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(64 * W, D > 128 && H == 1 ? 1 : (sizeof(T) == 2 && D == 128 && KT == 32 ? 3 : 2)) void attn_prompt_kernel(PromptArgs a) {
   using L = Tile<T, D, KT>;
   static_assert((S == 1 || KT == 32 * S) && (H == 1 || (S == 1 && KT == 32)));
   constexpr bool kF32T = std::is_same_v<T, float>;
@@ -563,7 +563,14 @@ hipError_t prompt_w(const PromptArgs& a, hipStream_t s) {
     constexpr int kWide = kF32 && D > 64 ? 32 : 64;
     // keys of a tile that is shared out over wavefronts: as many as LDS holds
     constexpr int kNarrow = D <= 128 ? 128 : 64;
-    return few ? run<T, D, kNarrow / 32, kNarrow, kNarrow / 32, 1>(a, s) : run<T, D, 4, kWide, 1, 1>(a, s);
+    if (few) return run<T, D, kNarrow / 32, kNarrow, kNarrow / 32, 1>(a, s);
+    if constexpr (!kF32 && D == 128) {
+      // Tiles of 32 keys leave room for a third workgroup on a CU, which works while others start or end: better for
+      // several rounds of short sequences (16 of 512 rows, 32 / 8 heads bf16: 73 us, with 64 keys 88; 6 of 1000: 71, 76), not
+      // for long ones (6000: 301, 289) nor for one round (2 of 1250: 46, 42).
+      if (a.b.n_q * a.b.n_heads >= kManyGroups * kCols && a.b.n_k <= 4096 * int64_t(a.b.n_seq)) return run<T, D, 4, 32, 1, 1>(a, s);
+    }
+    return run<T, D, 4, kWide, 1, 1>(a, s);
   }
 }
 

@@ -623,6 +623,13 @@ def test_prompt_wide_masks_and_chunks(torch_cuda, dtype, dim, causal, window):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 77), (False, 0)])
+def test_prompt_many_columns(torch_cuda, dtype, causal, window):
+    """Several rounds of workgroups: 4100 and more wavefronts of 32 columns."""
+    _prompt_case(torch_cuda, 35, dtype, 128, 2, 128, [300, 1, 0, 257, 300, 200], causal=causal, window=window)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("dim", DIMS)
 @pytest.mark.parametrize("heads", [2, 64])
 def test_prompt_nan_stays_where_it_is_seen(torch_cuda, dtype, dim, heads):
