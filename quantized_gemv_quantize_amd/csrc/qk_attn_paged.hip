@@ -30,9 +30,9 @@
 // Bound by memory and, close behind, by the vector instructions that take the codes apart (about 320 a
 // wavefront for 32 positions of 128 dims, 9 KB / us of cache for each SIMD).  Measured: 64 sequences of 61 .. 8190 on
 // 32 / 8 heads of 128 bf16, 314 MB: 78 us, 4.0 TB/s (a copy of 1 GiB reaches 5.0), of which the first
-// product starts after 5 us and the join takes 5; one sequence of 65502 (75 MB, f16): 28 us; of 317: 11 us.
+// product starts after 5 us and the join takes 5; one sequence of 65502 (75 MB, f16): 28 us; of 317: 10 us.
 //
-// Work is split over the positions when the table allows more than kDirectSteps steps: all
+// Work is split over the positions when the table allows more than kDirectPositions positions: all
 // items' steps laid end to end are cut into equal ranges, one a workgroup, however uneven
 // the sequences; ranges that hold a part of an item write (ref, sum, output) to the workspace and a
 // second kernel joins them.
@@ -45,9 +45,12 @@
 namespace qk {
 namespace {
 
-constexpr int kWaves = 4, kTile = 32, kStep = kWaves * kTile, kCols = 16;
-// 1024 positions: one sequence of 500, 900, 1500 takes 13, 18, 23 us whole and 17 each cut
-constexpr int kDirectSteps = 8;
+constexpr int kWaves = 4, kTile = 32, kCols = 16;
+// Positions a table may allow for whole items: one sequence of 500, 900, 1500 takes 13, 18, 23 us whole and 17 each cut.
+constexpr int kDirectPositions = 1024;
+// Items (as counted by max_items) up to which a workgroup of the whole form has 8 wavefronts, one workgroup to a CU:
+// 16 x 8, 32 x 8, 64 x 8 items of 500 positions take 11.9, 13.7, 25.0 us with 8 and 13.2, 14.7, 17.1 with 4.
+constexpr int64_t kFewItems = 320;
 constexpr int kFixedUnits = 3;   // an item's start and end cost about as much as 3 of its steps (1 .. 4: 104, 98, 95, 94 us for 64 sequences of 61 .. 8190)
 // least units of a range: 3, 6, 8, 12 measured 23, 26, 26, 31 us (16 sequences of 2 .. 6 rows, window 2048) and
 // 31, 31, 34, 36 (one sequence of 65502)
@@ -65,6 +68,7 @@ struct PagedArgs {
   JoinTask* tasks;  // workspace of the split (n_wg tasks, then the parts), null: one whole item to a workgroup
   int64_t q_stride, window;
   int n_heads, group, n_wg;
+  uint32_t step;  // positions that a workgroup's wavefronts take at a time
   float scale;
 };
 
@@ -99,7 +103,7 @@ __device__ __forceinline__ SeqWork seq_work(const PagedArgs& a, int64_t i) {
   if (hi <= lo) hi = lo = 0;
   s.lo = static_cast<int>(lo) & -kTile;
   s.hi = static_cast<int>(hi);
-  s.units = static_cast<int>((static_cast<uint32_t>(s.hi - s.lo) + kStep - 1) / kStep) + kFixedUnits;
+  s.units = static_cast<int>((static_cast<uint32_t>(s.hi - s.lo) + a.step - 1) / a.step) + kFixedUnits;
   return s;
 }
 
@@ -288,8 +292,9 @@ __device__ __forceinline__ void store_out(const PagedArgs& a, int64_t row0, int 
   for (int i = 0; i < 4; ++i) p[out_dim(b, e, i, g)] = static_cast<T>(v[i] * inv);
 }
 
-template <typename T, int D>
-__global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) void attn_paged_kernel(PagedArgs a) {
+// W wavefronts, each with every W-th 32 positions of the item.
+template <typename T, int D, int W>
+__global__ __launch_bounds__(64 * W, W == kWaves ? groups_per_cu(D, std::is_same_v<T, float>) : 2) void attn_paged_kernel(PagedArgs a) {
   constexpr int NB = D / 32, kRegs = NB * 2;  // float4 registers of the output
   constexpr bool kF32T = std::is_same_v<T, float>, kBf16T = std::is_same_v<T, bf16>;
   constexpr int P = kF32T ? 2 : 1;  // f16 pieces of a query and of a weight
@@ -297,13 +302,14 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
   // the type's precision: 2 pieces to 2^-21 (the second's last place is 2^-24), 8 bits for bf16; f16 is what it is
   constexpr float kPast = kF32T ? 2.0f : 8.0f, kLeast = kF32T ? 0x1p-4f : (kBf16T ? 0x1p-17f : 0.0f);
   // A wavefront's LDS: two tiles on their way from memory (each two halves of K codes, V codes, K
-  // scales, V scales), and in the same place its output registers for the joining of the four.
+  // scales, V scales), and in the same place its output registers for the joining.
   constexpr int kHalfBytes = 18 * D, kTileBytes = 2 * kHalfBytes, kWaveBytes = 2 * kTileBytes;
   static_assert(kRegs * 1024 <= kWaveBytes);
-  __shared__ uint4v lds[kWaves * (kWaveBytes + 512) / 16];
+  __shared__ uint4v lds[W * (kWaveBytes + 512) / 16];
   // One array on purpose: with several the compiler sees LDS loads that may alias each other and waits for all
   // loads before it reads any.
-  auto sref = reinterpret_cast<float(*)[64]>(lds + kWaves * kWaveBytes / 16), sl = sref + kWaves;
+  auto sref = reinterpret_cast<float(*)[64]>(lds + W * kWaveBytes / 16), sl = sref + W;
+  constexpr int kStep = W * kTile;
   const KvBatch& b = a.b;
   const int lane = threadIdx.x & 63, wave = wave_id(), col = lane % 16, g = lane / 16;
   const int64_t tokens = int64_t(1) << b.page_shift, half = kv_half_bytes(tokens, D);
@@ -649,17 +655,17 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
       }
     }
 
-    // the four wavefronts' states into one: each takes a quarter of the output registers
+    // the wavefronts' states into one: each takes its share of the output registers
     st.l = rows_sum(st.l);
     sref[wave][lane] = st.ref, sl[wave][lane] = st.l;
 #pragma unroll
     for (int i = 0; i < kRegs; ++i) reinterpret_cast<float4v*>(ring)[i * 64 + lane] = st.o[i / 2][i % 2];
     __syncthreads();
-    float ref = sref[0][lane], l = 0.0f, f[kWaves];
+    float ref = sref[0][lane], l = 0.0f, f[W];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) ref = fmaxf(ref, sref[w][lane]);
+    for (int w = 1; w < W; ++w) ref = fmaxf(ref, sref[w][lane]);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
       f[w] = __builtin_amdgcn_exp2f(sref[w][lane] - ref);
       l += sl[w][lane] * f[w];
     }
@@ -675,10 +681,10 @@ __global__ __launch_bounds__(256, groups_per_cu(D, std::is_same_v<T, float>)) vo
         a.tasks[blockIdx.x] = JoinTask{s.row0, tile, s.rows, kv, static_cast<int32_t>(w - blockIdx.x + 1), slot};
       }
     }
-    for (int i = wave; i < kRegs; i += kWaves) {
+    for (int i = wave; i < kRegs; i += W) {
       float4v v = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += reinterpret_cast<const float4v*>(lds)[w * (kWaveBytes / 16) + i * 64 + lane] * f[w];
+      for (int w = 0; w < W; ++w) v += reinterpret_cast<const float4v*>(lds)[w * (kWaveBytes / 16) + i * 64 + lane] * f[w];
       if (whole) {
         store_out<T, D>(a, s.row0, s.rows, tile, kv, i / 2, i % 2, v, inv);
       } else if (real) {
@@ -754,17 +760,26 @@ int64_t max_items(const KvBatch& b, int n_heads) {
   return (b.n_rows * (n_heads / b.n_kv) / kCols + seqs) * b.n_kv;
 }
 
-bool is_split(const KvBatch& b) { return (b.max_pages << b.page_shift) > kDirectSteps * kStep; }
+bool is_split(const KvBatch& b) { return (b.max_pages << b.page_shift) > kDirectPositions; }
 
 template <typename T, int D>
-hipError_t run(const PagedArgs& a, hipStream_t s) {
+hipError_t run(PagedArgs a, hipStream_t s) {
+  a.step = kWaves * kTile;
   if (a.tasks == nullptr) {
     unsigned gx = 0;
-    if (!launch_grid(max_items(a.b, a.n_heads), 256, &gx)) return hipErrorInvalidConfiguration;
-    attn_paged_kernel<T, D><<<gx, 256, 0, s>>>(a);
+    const int64_t items = max_items(a.b, a.n_heads);
+    if (!launch_grid(items, 512, &gx)) return hipErrorInvalidConfiguration;
+    if constexpr (D <= 128) {  // more dims leave no registers for two wavefronts to a SIMD
+      if (items <= kFewItems) {
+        a.step = 8 * kTile;
+        attn_paged_kernel<T, D, 8><<<gx, 512, 0, s>>>(a);
+        return hipGetLastError();
+      }
+    }
+    attn_paged_kernel<T, D, kWaves><<<gx, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
   }
-  attn_paged_kernel<T, D><<<a.n_wg, 256, 0, s>>>(a);
+  attn_paged_kernel<T, D, kWaves><<<a.n_wg, 64 * kWaves, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   attn_join_kernel<T, D><<<dim3(a.n_wg, D / 32), 256, 0, s>>>(a);
@@ -790,7 +805,7 @@ int64_t attn_paged_ws_bytes(const KvBatch& b, int dim, int) {
 hipError_t launch_attn_paged(const KvBatch& b, int dim, int dtype, const uint8_t* pages, const void* q, int64_t q_stride,
                              int n_heads, float scale, int64_t window, void* out, void* ws, hipStream_t s) {
   const PagedArgs a{b, pages, q, out, is_split(b) ? static_cast<JoinTask*>(ws) : nullptr, q_stride, window, n_heads,
-                    n_heads / b.n_kv, split_groups(dim, dtype == kF32), scale};
+                    n_heads / b.n_kv, split_groups(dim, dtype == kF32), 0, scale};
   switch (dtype) {
     case kF32: return paged_t<float>(a, dim, s);
     case kF16: return paged_t<_Float16>(a, dim, s);

@@ -392,6 +392,15 @@ def test_paged_garbage_in_masked_places(torch_cuda, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+def test_paged_many_short_sequences(torch_cuda, dtype, dim):
+    """A table too short for ranges, items too many for the widest workgroups."""
+    rng = np.random.default_rng(90)
+    new, start = [int(x) for x in rng.integers(0, 3, 70)], [int(x) for x in rng.integers(0, 300, 70)]
+    _paged_case(torch_cuda, 17, dtype, dim, 8, 8, 32, new, start)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n_seq", [65, 150])
 def test_paged_many_sequences_shared_out(torch_cuda, dtype, n_seq):
     """More sequences than a wavefront has lanes, empty ones among them, long enough to be cut into ranges:
