@@ -1,8 +1,8 @@
 // qk_attn_paged.hip - attention of packed rows over the paged Q4_0 cache.
 //
 // One item is 16 (row, head of the group) pairs of one sequence that share a key / value
-// head.  A workgroup of 4 wavefronts walks the item's positions in steps of 128, 32 to
-// a wavefront, each with its own running softmax; the four are joined through LDS at the end.
+// head.  A workgroup of 4 wavefronts (8 where items are few) walks the item's positions in steps of
+// 128 (256), 32 to a wavefront, each with its own running softmax; they are joined through LDS at the end.
 //
 // Both products run on mfma_16x16x32_f16 with q as the columns, so a lane's column (lane % 16)
 // and with it the softmax state stay the same throughout:
