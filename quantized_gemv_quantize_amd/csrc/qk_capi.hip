@@ -128,6 +128,10 @@ constexpr int64_t kMaxRows = INT32_MAX / 1024;
 // Row strides of the float tensors, in elements (32 times the widest row): with kMaxRows a byte offset stays far inside 64 bits.
 constexpr int64_t kMaxStride = int64_t(1) << 23;
 
+// A window no narrower than any two positions are apart (both below 2^32) hides nothing: none is the same, and
+// keeps the kernels' differences inside 64 bits.
+int64_t effective_window(int64_t window) { return window >= (int64_t(1) << 32) ? 0 : window; }
+
 // One float operand: rows of `width` elements `stride` apart.
 int check_rows(const void* p, int64_t stride, int64_t width, int64_t es) {
   if (stride < width || stride > kMaxStride) return QK_E_SHAPE;
@@ -440,7 +444,7 @@ int qk_attn_paged(const qk_kv_batch* batch, const void* pages, int dtype, const 
   if (need > 0 && !aligned16(ws)) return QK_E_ALIGN;
   if (ws_bytes < need) return QK_E_ARG;
   return status_of(qk::launch_attn_paged(b, static_cast<int>(dim), dtype, static_cast<const uint8_t*>(pages), q, q_stride,
-                                         static_cast<int>(n_heads), scale, window, out, ws,
+                                         static_cast<int>(n_heads), scale, effective_window(window), out, ws,
                                          static_cast<hipStream_t>(stream)));
 }
 
@@ -465,7 +469,8 @@ int qk_attn_prompt(int dtype, const void* q, int64_t q_stride, const void* k, in
   }
   if ((rc = check_rows(out, width, width, es)) != QK_OK) return rc;
   if (overlaps(q, q_stride, out, width, n_q, es)) return QK_E_ARG;
-  const qk::PromptBatch b{cu_q, cu_k, q_stride, k_stride, v_stride, n_q, n_k, window, static_cast<int>(n_seq),
+  const qk::PromptBatch b{cu_q, cu_k, q_stride, k_stride, v_stride, n_q, n_k, effective_window(window),
+                          static_cast<int>(n_seq),
                           static_cast<int>(n_heads), static_cast<int>(n_kv_heads), causal};
   return status_of(qk::launch_attn_prompt(b, static_cast<int>(head_dim), dtype, q, k, v, scale, out,
                                           static_cast<hipStream_t>(stream)));

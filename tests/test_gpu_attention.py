@@ -541,6 +541,31 @@ def test_calls_take_a_stream(torch_cuda):
         assert torch.equal(a, b)
 
 
+def test_widest_windows_hide_nothing(torch_cuda):
+    torch = torch_cuda
+    rng = np.random.default_rng(91)
+    c = Cache(torch, rng, [90, 40], 2, 64, 16)
+    q, k, v = (torch.randn(60, h, 64, device="cuda") for h in (4, 2, 2))
+    cu, start = i32(torch, [0, 3, 4]), i32(torch, [80, -2])
+    cu_q, cu_k = i32(torch, [0, 50, 60]), i32(torch, [0, 20, 60])
+    for window in (2 ** 32 - 1, 2 ** 32, 2 ** 62, 2 ** 63 - 1):
+        at = (c.pages, 16, c.dtable, cu, start, q[:4])
+        assert torch.equal(qk.qk_attn_paged(*at, window=window), qk.qk_attn_paged(*at))
+        assert torch.equal(qk.qk_attn_prompt(q, k, v, cu_q, cu_k, window=window), qk.qk_attn_prompt(q, k, v, cu_q, cu_k))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_paged_random(torch_cuda, seed):
+    rng = np.random.default_rng(5000 + seed)
+    hk = int(rng.choice([1, 2, 3, 4]))
+    h = hk * int(rng.choice([1, 2, 3, 5, 8, 16]))
+    n = int(rng.integers(1, 9))
+    new = [int(x) for x in rng.integers(0, 12, n)]
+    start = [int(x) for x in rng.integers(0, int(rng.choice([40, 400, 3000])), n)]
+    _paged_case(torch_cuda, 6000 + seed, str(rng.choice(TYPES)), int(rng.choice(DIMS)), hk, h, int(rng.choice([16, 32, 64, 128, 256])),
+                new, start, window=int(rng.choice([0, 0, 7, 200])), strided=bool(rng.integers(2)))
+
+
 # ---------------------------------------------------------------------------
 # attention over prompts
 
@@ -670,6 +695,18 @@ def test_prompt_peaked_and_flat(torch_cuda, dtype):
 def test_prompt_many_sequences(torch_cuda):
     rng = np.random.default_rng(29)
     _prompt_case(torch_cuda, 29, "bf16", 64, 1, 2, list(rng.integers(0, 40, 140)))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_prompt_random(torch_cuda, seed):
+    rng = np.random.default_rng(7000 + seed)
+    hk = int(rng.choice([1, 2, 3, 8]))
+    h = hk * int(rng.choice([1, 2, 3, 4, 7]))
+    n = int(rng.integers(1, 7))
+    lens = [int(x) for x in rng.integers(0, 350, n)]
+    klens = [int(x) for x in rng.integers(0, 500, n)] if rng.integers(2) else None
+    _prompt_case(torch_cuda, 8000 + seed, str(rng.choice(TYPES)), int(rng.choice(DIMS)), hk, h, lens, klens,
+                 causal=bool(rng.integers(3)), window=int(rng.choice([0, 0, 5, 90])), strided=klens is None and bool(rng.integers(2)))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
